@@ -24,3 +24,12 @@ from .api import (  # noqa: F401
     pisa_tail_score_histogram,
     pisa_workspace_bytes,
 )
+from .packed import (  # noqa: F401
+    pisa_page_plan,
+    pisa_page_write,
+    pisa_paged_attention,
+    pisa_paged_step,
+    pisa_varlen_attention,
+    pisa_varlen_attention_bwd,
+    varlen_attention,
+)

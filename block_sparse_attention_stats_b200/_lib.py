@@ -24,6 +24,9 @@ PISA_MODE_0TH = 1
 PISA_MODE_1ST = 2
 PISA_BF16 = 0
 PISA_F32 = 1
+PISA_F16 = 2
+PISA_CAUSAL = 1
+PISA_ZERO_TAIL = 2
 PISA_SINK_NONE = -(2 ** 31)
 
 # every exported symbol of include/pisa.h, with (restype, argtypes)
@@ -36,6 +39,28 @@ class PisaOptions(ctypes.Structure):
                 ("ws_bytes", ctypes.c_size_t), ("fuse_select", ctypes.c_int),
                 ("idx_out", ctypes.c_void_p)]
 
+
+class PisaRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("head_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
+class PisaPages(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+class PisaPageStep(ctypes.Structure):
+    _fields_ = [("past_lens", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("T", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("width", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("free_pages", ctypes.c_void_p), ("free_cap", ctypes.c_int),
+                ("num_free", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("num_free_out", ctypes.c_void_p)]
+
+
+_R, _G, _S = PisaRows, PisaPages, ctypes.POINTER(PisaPageStep)
 
 SIGNATURES = {
     "pisa_num_blocks": (_I, [_I, _I]),
@@ -64,6 +89,19 @@ SIGNATURES = {
     "pisa_selftest_timeout": (_I, [ctypes.c_uint64, _P]),
     "pisa_tail_score_histogram": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I,
                                        _I, _P, _P, _P, _P]),
+    "pisa_varlen_attention_workspace_bytes": (_Z, [_I, _I, _I]),
+    "pisa_varlen_attention": (_I, [_R, _R, _R, _I, _P, _I, _I, _I, _I, _I, _F, _I, _R, _P, _P,
+                                   _P, _Z, _P]),
+    "pisa_varlen_attention_bwd_workspace_bytes": (_Z, [_I, _I, _I, _I]),
+    "pisa_varlen_attention_bwd": (_I, [_R, _R, _R, _R, _I, _P, _P, _P, _I, _I, _I, _I, _I, _F,
+                                       _I, _R, _R, _R, _P, _Z, _P]),
+    "pisa_paged_attention_workspace_bytes": (_Z, [_I, _I, _I]),
+    "pisa_paged_attention": (_I, [_R, _G, _G, _I, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I,
+                                  _F, _R, _P, _P, _Z, _P]),
+    "pisa_page_plan": (_I, [_S, _P]),
+    "pisa_page_write": (_I, [_R, _R, _I, _P, _I, _I, _I, _G, _G, _I, _I, _P]),
+    "pisa_paged_step": (_I, [_S, _R, _R, _R, _G, _G, _I, _I, _I, _I, _I, _F, _R, _P, _P, _Z,
+                             _P]),
     "pisa_device_status": (_I, [_P]),
     "pisa_status_string": (ctypes.c_char_p, [_I]),
     "pisa_last_error": (ctypes.c_char_p, []),

@@ -1,0 +1,392 @@
+// Attention of a few packed rows (decoding: one or a few new tokens a request)
+// over a paged key/value cache.
+//
+// For row r of a unit (token i of n new ones of a request with m positions):
+//   o_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = exp(s q_r . k_j),  j <= m - n + i
+// in one pass over the keys with the running maximum and sum of the softmax.
+// Bound: HBM.  Every live page is read once; at R = 16 rows a key costs 2 D
+// bytes x 2 and 4 D R flops, 16 flops a byte, far under the tensor cores' 240.
+// So the kernel is built around the loads: one warp brings pages by TMA into a
+// ring that holds most of an SM's shared memory (three 64 KB tiles of 128 keys
+// at D = 128), eight warps work on the tiles, and the key range of the whole
+// batch is cut evenly over the SMs (packed_schedule.cuh), so one long request
+// and a batch of short ones both fill the machine.
+//
+// Per tile, warp w forms S for keys 16 w .. 16 w + 15 (mma.sync m16n8k16; the
+// rows are 16 at least, which a 128-row tcgen05 product would fill to an eighth,
+// and its accumulator would cross TMEM for every key), the warps agree on the
+// row maxima and lay down P (16-bit) through shared memory, and warp w adds
+// P V for its own D / 8 output columns, so the output needs no merge of warps.
+#pragma once
+
+#include "packed_schedule.cuh"
+#include "packed_primitives.cuh"
+
+namespace pisa {
+
+template <int D, int R> struct RowsCfg {
+  static constexpr int kConsumers = 256, kThreads = 288;
+  static constexpr int kBoxBytes = kKeyTile * 128;          // 64 columns x 128 keys
+  static constexpr int kTileBytes = kKeyTile * D * 2;       // K or V of a tile
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kQBytes = R * D * 2, kPBytes = R * kKeyTile * 2;
+  static constexpr int kFixed = kQBytes + kPBytes + 8 * R * 4 + 1024;
+  static constexpr int kMaxStages = (227 * 1024 - 1024 - kFixed) / kStageBytes;
+  static constexpr int kStages = kMaxStages < 6 ? kMaxStages : 6;
+  static constexpr int kOffQ = kStages * kStageBytes;
+  static constexpr int kOffP = kOffQ + kQBytes;
+  static constexpr int kOffRed = kOffP + kPBytes;           // [8][R] f32
+  static constexpr int kOffMisc = kOffRed + 8 * R * 4;      // barriers, schedule
+  static constexpr int kSmem = kOffMisc + 1024 + 1024;      // + alignment slack
+  static_assert(kStages >= 2 && kSmem <= 227 * 1024, "shared memory");
+};
+
+// Pages of a key/value cache as the loads see them.
+struct PagedKV {
+  const int32_t *table;      // [B, width]
+  int width, page_size, num_pages;
+};
+
+// Issues the copies of one tile's pages: keys key0 .. key0 + 127 of request b
+// that lie below kv, into `dst` (K, then V `v_off` bytes on).  All 32 lanes;
+// lane i brings the i-th page, whose number `page` it already holds.
+// Pages hold `rows` = min(page_size, 128) of the tile's keys each.  A page
+// number outside the cache reads as zeros (the copy's own bounds check).
+template <int D>
+__device__ __forceinline__ void issue_pages(const CUtensorMap *mk, const CUtensorMap *mv, uint32_t bar,
+                                            uint32_t dst, uint32_t v_off, int box_bytes, int key0,
+                                            int kv, int head, int page, int rows, int page_size,
+                                            int lane) {
+  const int live = kv - key0 <= 0 ? 0 : min((kv - key0 + rows - 1) / rows, kKeyTile / rows);
+  if (lane == 0) sm100::mbar_expect_tx(bar, (uint32_t)(live * rows * D * 2 * (v_off ? 2 : 1)));
+  __syncwarp();
+  if (lane < live) {
+    const int row = (key0 + lane * rows) % page_size;
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+      const uint32_t d = dst + b * box_bytes + lane * rows * 128;
+      sm100::tma_load_4d(d, mk, bar, 64 * b, row, head, page);
+      if (v_off) sm100::tma_load_4d(d + v_off, mv, bar, 64 * b, row, head, page);
+    }
+  }
+  __syncwarp();
+}
+
+// Page number of lane's page of the tile at key0, or -1 where there is none.
+__device__ __forceinline__ int lane_page(const PagedKV &c, int b, int key0, int kv, int rows, int lane) {
+  const int key = key0 + lane * rows;
+  if (lane >= kKeyTile / rows || key >= kv) return -1;
+  const int page = __ldg(c.table + (size_t)b * c.width + key / c.page_size);
+  if (page < 0 || page >= c.num_pages) {
+    report_device_error(kDevErrRange);
+    return -1;
+  }
+  return page;
+}
+
+template <typename T> __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
+                                                                uint32_t b0, uint32_t b1) {
+  if constexpr (Half16<T>::kBf16)
+    mma_bf16_16816(c, a, b0, b1);
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
+    attend_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PackedProblem p,
+                       const PagedKV cache, const T *__restrict__ q, long long q_head,
+                       long long q_row, float scale, const PackedOut o, PackedCut *__restrict__ cuts,
+                       float *__restrict__ part) {
+  using C = RowsCfg<D, R>;
+  using namespace sm100;
+  constexpr int RT = R / 16;            // m16 tiles
+  constexpr int NT = D / 64;            // n8 tiles of a warp's output columns
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char *smem = smem_raw + (sbase - raw);
+  const uint32_t bars = sbase + C::kOffMisc;                       // full[s], empty[s]
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 8 * (C::kStages + s); };
+  PackedStart *start = reinterpret_cast<PackedStart *>(smem + C::kOffMisc + 128);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 256);
+  long long *wsum = reinterpret_cast<long long *>(smem + C::kOffMisc + 384);   // 9 warps
+  float *red = reinterpret_cast<float *>(smem + C::kOffRed);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 8);
+    }
+    fence_mbar_init();
+    *abort = 0;
+    cuts[blockIdx.x].valid = 0;
+  }
+  if (tid == 32) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  packed_locate<RowCost<kKeyTile>>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
+  PackedWalk<RowCost<kKeyTile>> w;
+  w.begin(p, *start);
+  const int page_rows = min(cache.page_size, kKeyTile);
+
+  if (warp == 8) {
+    // ======================= page loads =======================================
+    int it = 0;
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const PackedSegment &s = w.s;
+      int page = lane_page(cache, s.b, s.ta * kKeyTile, s.r.kv, page_rows, lane);
+      for (int t = s.ta; t < s.tb; ++t, ++it) {
+        const int st = it % C::kStages;
+        if (it >= C::kStages &&
+            !__all_sync(0xffffffffu, mbar_wait(empty(st), ((it / C::kStages) - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (__any_sync(0xffffffffu, *abort != 0)) {
+          ok = false;
+          break;
+        }
+        issue_pages<D>(&tm_k, &tm_v, full(st), sbase + st * C::kStageBytes, C::kTileBytes,
+                       C::kBoxBytes, t * kKeyTile, s.r.kv, s.h, page, page_rows, cache.page_size,
+                       lane);
+        page = t + 1 < s.tb
+                   ? lane_page(cache, s.b, (t + 1) * kKeyTile, s.r.kv, page_rows, lane)
+                   : -1;
+      }
+    }
+    if (!ok) *abort = 1;
+    // copies in flight land before the CTA exits, whatever the consumers do
+    for (int i = max(it - C::kStages, 0); i < it; ++i) mbar_wait(full(i % C::kStages), (i / C::kStages) & 1);
+    return;
+  }
+
+  // ======================= the eight working warps ============================
+  const float sl2 = scale * kLog2e;
+  const int g = lane >> 2, c2 = (lane & 3) * 2;
+  int it = 0;
+  while (w.next(p)) {
+    const PackedSegment s = w.s;
+    const int tok0 = s.rt * p.tq, rows = min(s.r.n - tok0, p.tq) * p.G;
+    // Q of the unit: rows past the tile's are zero
+    consumers_sync();
+    for (int e = tid; e < R * (D / 8); e += C::kConsumers) {
+      const int row = e / (D / 8), ch = e % (D / 8);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows)
+        v = *reinterpret_cast<const uint4 *>(q + (long long)(s.h * p.G + row % p.G) * q_head +
+                                             (long long)(s.r.first + tok0 + row / p.G) * q_row + 8 * ch);
+      *reinterpret_cast<uint4 *>(smem + C::kOffQ + SwizzledTile<D>::offset(row, 8 * ch)) = v;
+    }
+    // keys each of this thread's rows sees: positions below lim
+    int lim[RT][2];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = 16 * i + g + 8 * x;
+        lim[i][x] = row >= rows ? 0
+                    : p.causal  ? max(min(s.r.past + tok0 + row / p.G + 1, s.r.kv), 0)
+                                : s.r.kv;
+      }
+    float m[RT][2], l[RT][2], acc[RT][NT][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[i][n][x] = 0.f;
+    }
+    consumers_sync();
+    for (int t = s.ta; t < s.tb; ++t, ++it) {
+      const int st = it % C::kStages;
+      // a warp that gives up goes on through the same barriers, so that no other waits for it;
+      // its results are not used: the error word says so
+      if (!__any_sync(0xffffffffu, *abort != 0) &&
+          !__all_sync(0xffffffffu, mbar_wait(full(st), (it / C::kStages) & 1)))
+        *abort = 1;
+      const uint32_t ks = sbase + st * C::kStageBytes, vs = ks + C::kTileBytes;
+      const int key0 = t * kKeyTile;
+      const int live = s.r.kv - key0;    // keys of the tile that exist
+      if (live < kKeyTile) {
+        // the rest of V may hold anything: zero, so that 0 x Inf or NaN never reaches a sum
+        const int z0 = max(live, 0);
+        for (int e = tid; e < (kKeyTile - z0) * (D / 8); e += C::kConsumers) {
+          const int row = z0 + e / (D / 8), ch = e % (D / 8);
+          *reinterpret_cast<uint4 *>(smem + st * C::kStageBytes + C::kTileBytes + (ch >> 3) * C::kBoxBytes +
+                                     row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();
+      }
+      // S = Q K^T for this warp's 16 keys
+      float sc[RT][2][4];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[i][n][x] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        const int krow = 16 * warp + ((lane >> 4) << 3) + (lane & 7), kc = 2 * k + ((lane >> 3) & 1);
+        ldmatrix_x4(ks + (kc >> 3) * C::kBoxBytes + krow * 128 + (((kc & 7) ^ (krow & 7)) << 4), b[0],
+                    b[1], b[2], b[3]);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          uint32_t a[4];
+          ldmatrix_x4(sbase + C::kOffQ +
+                          SwizzledTile<D>::offset(16 * i + (lane & 15), 16 * k + (lane >> 4) * 8),
+                      a[0], a[1], a[2], a[3]);
+          mma_16816<T>(sc[i][0], a, b[0], b[1]);
+          mma_16816<T>(sc[i][1], a, b[2], b[3]);
+        }
+      }
+      // scores in units of log2; the row maximum of these 16 keys
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int key = key0 + 16 * warp + 8 * n + c2 + y;
+              float &v = sc[i][n][2 * x + y];
+              v = key < lim[i][x] ? v * sl2 : -INFINITY;
+              mx = fmaxf(mx, v);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          if ((lane & 3) == 0) red[warp * R + 16 * i + g + 8 * x] = mx;
+        }
+      consumers_sync();
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int row = 16 * i + g + 8 * x;
+          float mt = red[row];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) mt = fmaxf(mt, red[j * R + row]);
+          const float mn = fmaxf(m[i][x], mt);
+          const float base = mn == -INFINITY ? 0.f : mn;   // no key seen yet: every weight is zero
+          const float f = ex2_approx(m[i][x] - base);
+          m[i][x] = mn;
+          l[i][x] *= f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            acc[i][n][2 * x] *= f;
+            acc[i][n][2 * x + 1] *= f;
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            // P is rounded to 16 bits for the product (the tensor cores take no more); the sum
+            // keeps the float32 weights, so only the weights' own rounding enters the output
+            const float p0 = ex2_approx(sc[i][n][2 * x] - base);
+            const float p1 = ex2_approx(sc[i][n][2 * x + 1] - base);
+            l[i][x] += p0 + p1;
+            *reinterpret_cast<uint32_t *>(smem + C::kOffP +
+                                          SwizzledTile<kKeyTile>::offset(row, 16 * warp + 8 * n + c2)) =
+                Half16<T>::pack(p0, p1);
+          }
+        }
+      consumers_sync();
+      // O += P V for this warp's D / 8 columns
+#pragma unroll
+      for (int k = 0; k < kKeyTile / 16; k += (NT == 2 ? 1 : 2)) {
+        uint32_t b[4];
+        if (NT == 2) {
+          const int vrow = 16 * k + (lane & 15), vc = 2 * warp + (lane >> 4);
+          ldmatrix_x4_trans(vs + (vc >> 3) * C::kBoxBytes + vrow * 128 + (((vc & 7) ^ (vrow & 7)) << 4),
+                            b[0], b[1], b[2], b[3]);
+        } else {
+          const int vrow = 16 * k + lane;
+          ldmatrix_x4_trans(vs + vrow * 128 + ((warp ^ (vrow & 7)) << 4), b[0], b[1], b[2], b[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          uint32_t a[4];
+          const uint32_t prow = 16 * i + (lane & 15);
+          ldmatrix_x4(sbase + C::kOffP + SwizzledTile<kKeyTile>::offset(prow, 16 * k + (lane >> 4) * 8),
+                      a[0], a[1], a[2], a[3]);
+          mma_16816<T>(acc[i][0], a, b[0], b[1]);
+          if constexpr (NT == 2) {
+            mma_16816<T>(acc[i][1], a, b[2], b[3]);
+          } else {
+            ldmatrix_x4(sbase + C::kOffP +
+                            SwizzledTile<kKeyTile>::offset(prow, 16 * (k + 1) + (lane >> 4) * 8),
+                        a[0], a[1], a[2], a[3]);
+            mma_16816<T>(acc[i][0], a, b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(st));
+    }
+    // l over the 4 lanes of a row and the 8 warps
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[i][x] += __shfl_xor_sync(0xffffffffu, l[i][x], 1);
+        l[i][x] += __shfl_xor_sync(0xffffffffu, l[i][x], 2);
+        if ((lane & 3) == 0) red[warp * R + 16 * i + g + 8 * x] = l[i][x];
+      }
+    consumers_sync();
+    float *slot = part + ((size_t)blockIdx.x * 2 + s.slot()) * packed_slot_floats<D>(R);
+    const bool whole = s.whole();
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int row = 16 * i + g + 8 * x;
+        float ls = red[row];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) ls += red[j * R + row];
+        if (row >= rows) continue;
+        const bool head_lane = warp == 0 && (lane & 3) == 0;
+        if (whole) {
+          const float inv = ls > 0.f ? 1.f / ls : ls == 0.f ? 0.f : ls;
+          const int token = s.r.first + tok0 + row / p.G, head = s.h * p.G + row % p.G;
+          T *dst = reinterpret_cast<T *>(o.out) + head * o.head + token * o.row;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            *reinterpret_cast<uint32_t *>(dst + warp * (D / 8) + 8 * n + c2) =
+                Half16<T>::pack(acc[i][n][2 * x] * inv, acc[i][n][2 * x + 1] * inv);
+          if (head_lane && o.lse)
+            o.lse[(size_t)head * p.T + token] =
+                ls == 0.f ? -INFINITY : (m[i][x] + log2f(ls)) * 0.6931471805599453f;
+        } else {
+          if (head_lane) {
+            slot[row] = m[i][x];
+            slot[R + row] = ls;
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const int col = warp * (D / 8) + 8 * n + c2;
+            *reinterpret_cast<float2 *>(slot + 2 * R + ((size_t)(col >> 2) * R + row) * 4 + (col & 3)) =
+                make_float2(acc[i][n][2 * x], acc[i][n][2 * x + 1]);
+          }
+        }
+      }
+    if (!whole && s.ta == 0 && tid == 0) cuts[blockIdx.x] = packed_cut(*start, s);
+  }
+}
+
+}  // namespace pisa

@@ -1,0 +1,558 @@
+// Gradients of attention over packed sequences (causal or not, grouped heads),
+// on the sm_100a tensor cores.  With P_tj = exp(s q_t . k_j - lse_t), dP_tj =
+// dout_t . v_j and Delta_t = dout_t . o_t (= sum_j P_tj dP_tj):
+//   dq_t = s sum_j P_tj (dP_tj - Delta_t) k_j
+//   dk_j = s sum_t P_tj (dP_tj - Delta_t) q_t,   dv_j = sum_t P_tj dout_t
+// where t runs over the rows of every query head of the key head's group.
+// Bound: the tensor cores, seven products of 2 D flops a row and key (S and dP
+// are formed in both kernels).  One kernel with five would have to add dq from
+// every key tile: float32 atomics, whose order changes results, or a wait of
+// CTAs on one another.  Two kernels keep every sum in one CTA in a fixed order.
+//
+// Both keep a pair of 128-row tiles in shared memory (dq: Q and dout; dk, dv: K
+// and V) and stream the other pair through a ring, 128 rows at a time; both are
+// cut evenly over the SMs (packed_schedule.cuh), and sum_partials_kernel joins
+// what a range's end cuts.
+// Roles (320 threads): warp 0 copies; warp 1 issues every product; warps 2-5
+// take columns 0 .. 63 of each 128 x 128 tile, warps 6-9 columns 64 .. 127, one
+// thread a row (TMEM lane).
+// The order of products keeps the tensor cores busy while the tile's weights are
+// formed, without a second pair of accumulators:
+//   dq      S_0 dP_0 | S_u+1 (once S_u is in registers), dQ += dS_u K_u, dP_u+1 | ...
+//   dk, dv  S_0 dP_0 | dV += P_u dout_u, S_u+1, dK += dS_u Q_u, dP_u+1 | ...
+// so the exponentials of tile u + 1 overlap dQ_u and dP_u+1 (dK_u and dP_u+1),
+// and dS_u overlaps S_u+1.  16-bit dS is written over the dP columns it was
+// formed from, 16-bit P over its S columns, each warpgroup over its own (the A
+// operand of the next product reads each half where it lies).  An overwrite is
+// safe because one thread issues all products and they run in order.
+// Rounding: P and dS are rounded to bf16 for their products (the tensor cores
+// take no more), everything else is float32.
+#pragma once
+
+#include "packed_primitives.cuh"
+#include "packed_schedule.cuh"
+
+namespace pisa {
+
+// lse2 = lse log2 e and Delta, [Hq, T]: one warp a row
+template <int D>
+__global__ void __launch_bounds__(256)
+    packed_delta_kernel(const __nv_bfloat16 *__restrict__ dout, long long head_stride, long long row_stride,
+                        const float *__restrict__ out, const float *__restrict__ lse, int Hq, int T,
+                        const int32_t *__restrict__ cu, int B, float *__restrict__ lse2,
+                        float *__restrict__ delta) {
+  const int lane = threadIdx.x & 31;
+  const int end = min(max(__ldg(cu + B), 0), T);      // rows behind the last sequence are not read
+  const long long rows = (long long)Hq * T;
+  for (long long r = (blockIdx.x * 256ll + threadIdx.x) >> 5; r < rows; r += gridDim.x * 8ll) {
+    const int h = (int)(r / T), t = (int)(r % T);
+    if (t >= end) continue;
+    float s = 0.f;
+    if (lane < D / 4) {
+      const float4 o = reinterpret_cast<const float4 *>(out + r * D)[lane];
+      const uint2 g = *reinterpret_cast<const uint2 *>(dout + h * head_stride + t * row_stride + 4 * lane);
+      const float2 a = Half16<__nv_bfloat16>::unpack(g.x), b = Half16<__nv_bfloat16>::unpack(g.y);
+      s = fmaf(o.x, a.x, fmaf(o.y, a.y, fmaf(o.z, b.x, o.w * b.y)));
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (lane == 0) {
+      delta[r] = s;
+      lse2[r] = lse[r] * kLog2e;
+    }
+  }
+}
+
+template <int D> struct PackedBwdCfg {
+  static constexpr int kThreads = 320;
+  static constexpr int kRows = 128;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kBoxBytes = 128 * 128;
+  static constexpr int kOffA = 0;                          // the resident pair
+  static constexpr int kOffRing = 2 * kTileBytes;
+  static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
+  static constexpr int kVecs = D == 128 ? 4 : 6;           // lse and Delta of streamed rows (dk, dv)
+  static constexpr int kOffVec = kOffMisc + 512;
+  static constexpr int kSmem = kOffMisc + 512 + 1024;      // dq; + alignment slack
+  static constexpr int kStagesKv = D == 128 ? 4 : 8;       // dk, dv: one stage less makes room for them
+  static constexpr int kOffMiscKv = kOffRing + kStagesKv * kTileBytes;
+  static constexpr int kSmemKv = kOffMiscKv + 512 + kVecs * 1024 + 1024;
+  static_assert(kSmem <= 227 * 1024 && kSmemKv <= 227 * 1024, "shared memory");
+  static constexpr int kBarAFull = 0, kBarAEmpty = 1, kBarS = 2, kBarDP = 3, kBarP = 4, kBarZ = 5, kBarAcc = 6,
+                       kBarAccFree = 7, kBarTeardown = 8, kBarFull = 9, kBarEmpty = kBarFull + 8;
+  static_assert(kBarEmpty + 8 <= 32, "barrier slots");
+  static constexpr uint32_t kTmemCols = 512, kColS = 0, kColDP = 128, kColAcc = 256;
+};
+
+// KV = false: dq.  The unit's rows are 128 / G tokens with the G heads of a key
+// head (token-major), streamed pairs are K and V of a key tile.
+// KV = true: dk, dv.  The unit's rows are 128 keys, streamed pairs are Q and dout
+// of 128 tokens of one query head; tiles run over the heads, then the tokens.
+template <int D, bool KV>
+__global__ void __launch_bounds__(320, 1)
+    packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const PackedProblem p, float scale, const float *__restrict__ lse2,
+                      const float *__restrict__ delta, __nv_bfloat16 *__restrict__ out0,
+                      long long out0_head, long long out0_row, __nv_bfloat16 *__restrict__ out1,
+                      long long out1_head, long long out1_row, PackedCut *__restrict__ cuts,
+                      float *__restrict__ part) {
+  using C = PackedBwdCfg<D>;
+  using Cost = typename std::conditional<KV, KeyCost, RowCost<kKeyTile>>::type;
+  using namespace sm100;
+  constexpr int kStages = KV ? C::kStagesKv : C::kStages;
+  constexpr int kMisc = KV ? C::kOffMiscKv : C::kOffMisc;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  unsigned char *smem = smem_raw + (sbase - raw);
+  auto bar = [&](int i) -> uint32_t { return sbase + kMisc + 8 * i; };
+  PackedStart *start = reinterpret_cast<PackedStart *>(smem + kMisc + 256);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + kMisc + 320);
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + kMisc + 336);
+  long long *wsum = reinterpret_cast<long long *>(smem + kMisc + 384);
+  float *vec = reinterpret_cast<float *>(smem + kMisc + 512);      // [kVecs][lse 128, Delta 128] (KV)
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int sub_rows = KV ? 128 : p.tq * p.G;
+
+  if (warp == 1) {
+    tmem_alloc(sbase + kMisc + 336, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i <= C::kBarTeardown; ++i)
+      mbar_init(bar(i), i == C::kBarP || i == C::kBarZ || i == C::kBarAccFree ? 256 : 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(C::kBarFull + s), 1);
+      mbar_init(bar(C::kBarEmpty + s), 1);
+    }
+    fence_mbar_init();
+    *abort = 0;
+    cuts[blockIdx.x].valid = 0;
+  }
+  if (tid == 32) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_do);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (!KV)   // rows of the Q and dout tiles that no copy fills (128 is no multiple of G): zero
+    for (int e = tid; e < 2 * (128 - sub_rows) * (D / 8); e += C::kThreads) {
+      const int ch = e % (D / 8), row = sub_rows + (e / (D / 8)) % (128 - sub_rows),
+                i = e / ((D / 8) * (128 - sub_rows));
+      *reinterpret_cast<uint4 *>(smem + C::kOffA + i * C::kTileBytes + (ch >> 3) * C::kBoxBytes + row * 128 +
+                                 ((ch & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  fence_proxy_async();
+  tc_fence_before();
+  packed_locate<Cost>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  PackedWalk<Cost> w;
+  w.begin(p, *start);
+
+  auto uwait = [&](uint32_t b_addr, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(b_addr, parity));
+  };
+  auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort != 0); };
+  // streamed tile t of a unit: the query head inside the group (KV), the first
+  // token or key of its 128 rows
+  auto tile_at = [&](const PackedSegment &s, int t, int &g) -> int {
+    if (!KV) return t * 128;
+    const int per = s.nt / p.G;
+    g = t / per;
+    return (t % per + (p.causal ? s.rt : 0)) * 128;
+  };
+
+  if (warp == 0) {
+    // ======================= copies ============================================
+    int slot = 0, seg = 0, tile = 0;
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const PackedSegment &s = w.s;
+      if (aborted() || (seg > 0 && !uwait(bar(C::kBarAEmpty), (seg - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      if (elect_one()) {
+        const uint32_t a = bar(C::kBarAFull);
+        mbar_expect_tx(a, 2 * sub_rows * D * 2);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b) {
+            const uint32_t dst = sbase + C::kOffA + x * C::kTileBytes + b * C::kBoxBytes;
+            if (KV)
+              tma_load_3d(dst, x ? &tm_v : &tm_k, a, 64 * b, s.r.first + s.rt * 128, s.h);
+            else
+              tma_load_4d(dst, x ? &tm_do : &tm_q, a, 64 * b, 0, s.r.first + s.rt * p.tq, s.h);
+          }
+      }
+      __syncwarp();
+      ++seg;
+      for (int t = s.ta; ok && t < s.tb; ++t, ++tile) {
+        int g = 0;
+        const int row0 = tile_at(s, t, g);
+        const int head = KV ? s.h * p.G + g : s.h;
+#pragma unroll
+        for (int x = 0; x < 2; ++x, ++slot) {
+          const int st = slot % kStages;
+          if (aborted() || (slot >= kStages && !uwait(bar(C::kBarEmpty + st), ((slot / kStages) - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          if (KV && x == 0) {
+            // lse and Delta of the tile's rows, before the arrival that hands the slot over.
+            // Buffer tile % kVecs was last read for tile - kVecs, whose dS came before the
+            // products that freed this slot
+            float *v = vec + (tile % C::kVecs) * 256;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = lane + 32 * k;
+              const bool in = row0 + r < s.r.n;
+              const size_t at = (size_t)head * p.T + s.r.first + row0 + r;
+              v[r] = in ? lse2[at] : INFINITY;     // exp2(x - inf) = 0: a row that is not there
+              v[128 + r] = in ? delta[at] : 0.f;
+            }
+            __syncwarp();
+          }
+          if (elect_one()) {
+            const uint32_t dst = sbase + C::kOffRing + st * C::kTileBytes;
+            mbar_expect_tx(bar(C::kBarFull + st), C::kTileBytes);
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b)
+              tma_load_3d(dst + b * C::kBoxBytes, KV ? (x ? &tm_do : &tm_q) : (x ? &tm_v : &tm_k),
+                          bar(C::kBarFull + st), 64 * b, s.r.first + row0, head);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (!ok) {
+      *abort = 1;
+      // copies in flight land before the CTA exits
+      if (seg > 0) uwait(bar(C::kBarAFull), (seg - 1) & 1);
+      for (int i = max(slot - kStages, 0); i < slot; ++i)
+        uwait(bar(C::kBarFull + i % kStages), (i / kStages) & 1);
+    }
+  } else if (warp == 1) {
+    // ======================= products ==========================================
+    constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t kIdAcc = idesc_bf16_f32(128, D, 0, 1);
+    auto step = [](int k) -> uint64_t {
+      return (uint64_t)(((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4);
+    };
+    auto ring = [&](int sl) -> uint32_t { return sbase + C::kOffRing + (sl % kStages) * C::kTileBytes; };
+    auto commit = [&](int b) {
+      if (elect_one()) tc_commit(bar(b));
+      __syncwarp();
+    };
+    // waits for a ring slot; rows past the sequence's last may hold anything: zero, so that
+    // 0 x Inf or NaN never reaches a sum
+    auto take = [&](int sl, int live) -> bool {
+      if (!uwait(bar(C::kBarFull + sl % kStages), (sl / kStages) & 1)) return false;
+      if (live < 128) {
+        unsigned char *v = smem + C::kOffRing + (sl % kStages) * C::kTileBytes;
+        for (int e = lane; e < (128 - live) * (D / 8); e += 32) {
+          const int row = live + e / (D / 8), ch = e % (D / 8);
+          *reinterpret_cast<uint4 *>(v + (ch >> 3) * C::kBoxBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async();
+        __syncwarp();
+      }
+      tc_fence_after();
+      return true;
+    };
+    // S (x = 0) or dP (x = 1) of the tile whose pair starts at ring slot sl
+    auto issue_s = [&](int x, int sl) {
+      const uint64_t ad = smem_desc_sw128(sbase + C::kOffA + x * C::kTileBytes, 16, 1024);
+      const uint64_t bd = smem_desc_sw128(ring(sl + x), 16, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + (x ? C::kColDP : C::kColS), ad + step(k), bd + step(k), kIdS, k > 0 ? 1u : 0u);
+        tc_commit(bar(x ? C::kBarDP : C::kBarS));
+      }
+      __syncwarp();
+    };
+    // accumulator `a` += 16-bit tile at TMEM column `col` (two 64-wide halves) times ring slot sl
+    auto issue_acc = [&](int a, uint32_t col, int sl, bool first) {
+      const uint64_t bd = smem_desc_sw128(ring(sl), C::kBoxBytes, 1024);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts(tmem + C::kColAcc + D * a, tmem + col + (k >> 2) * 64 + (k & 3) * 8,
+                 bd + (uint64_t)((k * 2048) >> 4), kIdAcc, (!first || k > 0) ? 1u : 0u);
+      }
+      __syncwarp();
+    };
+    int slot = 0, seg = 0, u = 0;
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const PackedSegment &s = w.s;
+      int g = 0;
+      auto live = [&](int t) { return max(min(s.r.n - tile_at(s, t, g), 128), 0); };
+      if (aborted() || !uwait(bar(C::kBarAFull), seg & 1) || !take(slot, live(s.ta))) {
+        ok = false;
+        break;
+      }
+      issue_s(0, slot);
+      if (!take(slot + 1, live(s.ta))) {
+        ok = false;
+        break;
+      }
+      issue_s(1, slot);
+      if (!KV) commit(C::kBarEmpty + (slot + 1) % kStages);
+      if (s.ta + 1 == s.tb) commit(C::kBarAEmpty);
+      for (int t = s.ta; t < s.tb; ++t, slot += 2, ++u) {
+        const bool more = t + 1 < s.tb, first = t == s.ta;
+        // P_u of dk, dv is in TMEM; S_u of dq is in registers
+        if (aborted() || !uwait(bar(C::kBarP), u & 1)) {
+          ok = false;
+          break;
+        }
+        // the accumulators of the unit before have been read
+        if (first && seg > 0 && !uwait(bar(C::kBarAccFree), (seg - 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (KV) {
+          issue_acc(1, C::kColS, slot + 1, first);            // dV += P dout
+          commit(C::kBarEmpty + (slot + 1) % kStages);
+        }
+        if (more) {
+          if (!take(slot + 2, live(t + 1))) {
+            ok = false;
+            break;
+          }
+          issue_s(0, slot + 2);
+        }
+        if (!uwait(bar(C::kBarZ), u & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_acc(0, C::kColDP, slot, first);                 // dQ += dS K, or dK += dS Q
+        commit(C::kBarEmpty + slot % kStages);
+        if (more) {
+          if (!take(slot + 3, live(t + 1))) {
+            ok = false;
+            break;
+          }
+          issue_s(1, slot + 2);
+          if (!KV) commit(C::kBarEmpty + (slot + 3) % kStages);
+          if (t + 2 == s.tb) commit(C::kBarAEmpty);
+        } else {
+          commit(C::kBarAcc);
+        }
+      }
+      ++seg;
+    }
+    if (!ok) {
+      *abort = 1;
+      commit(C::kBarTeardown);
+      uwait(bar(C::kBarTeardown), 0);
+    }
+  } else {
+    // ======================= weights ===========================================
+    const int gw = (warp - 2) >> 2;              // columns 64 gw .. 64 gw + 63
+    const int sp = warp & 3;
+    const int row = sp * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(sp * 32) << 16);
+    const uint32_t s_addr = lane_addr + C::kColS + 64 * gw, dp_addr = lane_addr + C::kColDP + 64 * gw;
+    const float sl2 = scale * kLog2e;
+    int u = 0, seg = 0;
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const PackedSegment s = w.s;
+      int g = 0;
+      // dq: this row's token, lse and Delta.  dk, dv: this row's key
+      const int tok = KV ? s.rt * 128 + row : s.rt * p.tq + row / p.G;
+      const bool valid = tok < s.r.n && row < sub_rows;
+      const int qhead = s.h * p.G + row % p.G;
+      const size_t hr = (size_t)qhead * p.T + s.r.first + tok;
+      const float lrow = !KV && valid ? lse2[hr] : 0.f, drow = !KV && valid ? delta[hr] : 0.f;
+      for (int t = s.ta; t < s.tb; ++t, ++u) {
+        const int row0 = tile_at(s, t, g);
+        const float *ls = vec + (u % C::kVecs) * 256 + 64 * gw, *dl = ls + 128;
+        // visible columns [c0, c1) of this thread's 64
+        int c0 = 0, c1 = 64;
+        if (KV) {
+          if (p.causal) c0 = tok - row0 - 64 * gw;             // tokens at or behind the key
+        } else {
+          c1 = (p.causal ? min(tok, s.r.n - 1) + 1 : s.r.n) - row0 - 64 * gw;
+        }
+        if (aborted() || !uwait(bar(C::kBarS), u & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float pv[64];
+        {
+          uint32_t r[2][32];
+          tmem_ld_x32(s_addr, r[0]);
+          tmem_ld_x32(s_addr + 32, r[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 64; ++c) pv[c] = __uint_as_float(r[c >> 5][c & 31]);
+        }
+        if (!KV) {
+          tc_fence_before();
+          mbar_arrive(bar(C::kBarP));          // S may be overwritten
+        }
+        if (KV) {
+          // (the slot's arrival also hands over lse and Delta)
+          if (!uwait(bar(C::kBarFull + (2 * u) % kStages), (2 * u / kStages) & 1)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const float4 l4 = *reinterpret_cast<const float4 *>(ls + c);
+            pv[c] = ex2_approx(fmaf(pv[c], sl2, -l4.x));
+            pv[c + 1] = ex2_approx(fmaf(pv[c + 1], sl2, -l4.y));
+            pv[c + 2] = ex2_approx(fmaf(pv[c + 2], sl2, -l4.z));
+            pv[c + 3] = ex2_approx(fmaf(pv[c + 3], sl2, -l4.w));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) pv[c] = ex2_approx(fmaf(pv[c], sl2, -lrow));
+        }
+        if (__any_sync(0xffffffffu, c0 > 0 || c1 < 64)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) pv[c] = c >= c0 && c < c1 ? pv[c] : 0.f;
+        }
+        if (KV) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
+          tmem_st_x32(s_addr, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(C::kBarP));
+        }
+        if (aborted() || !uwait(bar(C::kBarDP), u & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        {
+          uint32_t r[2][32], pk[32];
+          tmem_ld_x32(dp_addr, r[0]);
+          tmem_ld_x32(dp_addr + 32, r[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            float4 d4 = make_float4(drow, drow, drow, drow);
+            if (KV) d4 = *reinterpret_cast<const float4 *>(dl + c);
+            pk[c / 2] = pack_bf16x2(pv[c] * (__uint_as_float(r[c >> 5][c & 31]) - d4.x),
+                                    pv[c + 1] * (__uint_as_float(r[c >> 5][(c & 31) + 1]) - d4.y));
+            pk[c / 2 + 1] = pack_bf16x2(pv[c + 2] * (__uint_as_float(r[c >> 5][(c & 31) + 2]) - d4.z),
+                                        pv[c + 3] * (__uint_as_float(r[c >> 5][(c & 31) + 3]) - d4.w));
+          }
+          tmem_st_x32(dp_addr, pk);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarZ));
+      }
+      if (!ok) break;
+      // ---- epilogue: dq = s dQ (half of the columns a warpgroup); dk = s dK, dv = dV (one each) ----
+      if (aborted() || !uwait(bar(C::kBarAcc), seg & 1)) {
+        ok = false;
+        break;
+      }
+      ++seg;
+      tc_fence_after();
+      const bool whole = s.whole();
+      constexpr int kCols = KV ? D : D / 2;
+      const int col0 = KV ? 0 : gw * (D / 2);
+      const float f = KV && gw == 1 ? 1.f : scale;
+      const uint32_t acc = lane_addr + C::kColAcc + (KV ? D * gw : col0);
+      // KV: warpgroup 0 holds dK (accumulator 0), warpgroup 1 dV (accumulator 1)
+      __nv_bfloat16 *dst = KV && gw == 1 ? out1 + s.h * out1_head + (long long)(s.r.first + tok) * out1_row
+                           : KV          ? out0 + s.h * out0_head + (long long)(s.r.first + tok) * out0_row
+                                         : out0 + qhead * out0_head + (long long)(s.r.first + tok) * out0_row;
+      float4 *ps = reinterpret_cast<float4 *>(part) +
+                   ((size_t)blockIdx.x * 2 + s.slot()) * ((KV ? 2 : 1) * 128 * (D / 4)) +
+                   (KV ? gw * 128 * (D / 4) : 0);
+#pragma unroll
+      for (int c = 0; c < kCols / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld_x32(acc + 32 * c, r);
+        tmem_wait_ld();
+        if (!valid) continue;
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = f * __uint_as_float(r[k]);
+        if (whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            reinterpret_cast<uint4 *>(dst + col0 + 32 * c)[k] =
+                make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                           pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            ps[(size_t)(col0 / 4 + 8 * c + k) * 128 + row] =
+                make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(C::kBarAccFree));
+      if (!whole && s.ta == 0 && tid == 64) cuts[blockIdx.x] = packed_cut(*start, s);
+    }
+    if (!ok) *abort = 1;
+  }
+
+  // ---- teardown -----------------------------------------------------------------
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the partial sums of the unit that CTA blockIdx.x's range cuts, in
+// ascending CTA order.  blockIdx.z: dk or dv (KV).
+template <int D, bool KV>
+__global__ void __launch_bounds__(256)
+    packed_sum_kernel(const PackedProblem p, const PackedCut *__restrict__ cuts, const float *__restrict__ part,
+                      __nv_bfloat16 *__restrict__ out0, long long out0_head, long long out0_row,
+                      __nv_bfloat16 *__restrict__ out1, long long out1_head, long long out1_row, int clear) {
+  if (clear)
+    clear_tail<D>(p, KV ? p.Hkv : p.Hq, blockIdx.z ? out1 : out0, blockIdx.z ? out1_head : out0_head,
+                  blockIdx.z ? out1_row : out0_row,
+                  ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                  (long long)gridDim.x * gridDim.y * blockDim.x);
+  const PackedCut cut = cuts[blockIdx.x];
+  if (!cut.valid) return;
+  const PackedRequest r = packed_request(p, cut.b);
+  const int per = KV ? 128 : p.tq, g = KV ? 1 : p.G, tok0 = cut.rt * per;
+  const int rows = min(r.n - tok0, per) * g;
+  const int c0 = blockIdx.x, n = cut.last - c0 + 1;
+  constexpr size_t kSlot = (size_t)(KV ? 2 : 1) * 128 * (D / 4);
+  const float4 *base = reinterpret_cast<const float4 *>(part) + blockIdx.z * (128 * (D / 4));
+  __nv_bfloat16 *out = blockIdx.z ? out1 : out0;
+  const long long hs = blockIdx.z ? out1_head : out0_head, rs = blockIdx.z ? out1_row : out0_row;
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 4); e += gridDim.y * blockDim.x) {
+    const int row = e / (D / 4), c4 = e % (D / 4);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; ++i) {
+      const float4 x = base[((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kSlot + (size_t)c4 * 128 + row];
+      a.x += x.x;
+      a.y += x.y;
+      a.z += x.z;
+      a.w += x.w;
+    }
+    const long long at = (cut.h * g + row % g) * hs + (long long)(r.first + tok0 + row / g) * rs + 4 * c4;
+    *reinterpret_cast<uint2 *>(out + at) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+}
+
+}  // namespace pisa

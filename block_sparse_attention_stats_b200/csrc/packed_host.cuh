@@ -1,0 +1,106 @@
+// Host-side helpers of the packed and paged entry points: argument checks and
+// tensor maps of strided 16-bit tensors.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <string>
+
+#include "pisa_common.cuh"
+
+namespace pisa {
+
+// CTAs of the persistent kernels: one per SM of a B200.  No CTA waits for
+// another, so any other number of SMs runs them too.
+constexpr int kPackedCtas = 148;
+
+#define PISA_TRY(expr)                         \
+  do {                                         \
+    pisa_status _s = (expr);                   \
+    if (_s != PISA_OK) return _s;              \
+  } while (0)
+
+#define PISA_CUDA(expr)                        \
+  do {                                         \
+    cudaError_t _e = (expr);                   \
+    if (_e != cudaSuccess) {                   \
+      set_last_error(_e);                      \
+      return PISA_ERR_CUDA;                    \
+    }                                          \
+  } while (0)
+
+inline bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// [H][T] rows of d elements at the given strides: 16-byte aligned, rows of one
+// tensor that is written must not share memory.  The stride of an extent of one
+// is never used.
+inline pisa_status check_rows(const pisa_rows &r, int H, int T, int d, bool written) {
+  if (!aligned16(r.data)) return PISA_ERR_INVALID_ARG;
+  if (H > 1 && (r.head_stride < d || r.head_stride % 8 || r.head_stride >= (1ll << 38)))
+    return PISA_ERR_INVALID_ARG;
+  if (T > 1 && (r.row_stride < d || r.row_stride % 8 || r.row_stride >= (1ll << 38)))
+    return PISA_ERR_INVALID_ARG;
+  if (written && H > 1 && T > 1 && r.head_stride < (int64_t)(T - 1) * r.row_stride + d &&
+      r.row_stride < (int64_t)(H - 1) * r.head_stride + d)
+    return PISA_ERR_INVALID_ARG;
+  return PISA_OK;
+}
+
+// 16-bit tensor of `rank` dimensions, innermost contiguous, read in boxes of 64
+// columns with the 128-byte swizzle; what lies outside reads as zero.
+inline pisa_status map16(CUtensorMap *m, const void *base, bool bf16, int rank, const uint64_t *dims,
+                         const uint64_t *stride_elems, const uint32_t *box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
+  if (!enc) {
+    set_last_error_text("cuTensorMapEncodeTiled is not available from the driver");
+    return PISA_ERR_CUDA;
+  }
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], e[4];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    e[i] = 1;
+    if (i) s[i - 1] = (dims[i] > 1 ? stride_elems[i] : dims[0]) * 2;   // an extent of one: any legal stride
+  }
+  const CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                         const_cast<void *>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_last_error_text("cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r));
+    return PISA_ERR_CUDA;
+  }
+  return PISA_OK;
+}
+
+// rows of one head: (column, row, head)
+inline pisa_status map_rows(CUtensorMap *m, const pisa_rows &r, bool bf16, int d, int T, int H, int box_rows) {
+  const uint64_t dims[3] = {(uint64_t)d, (uint64_t)T, (uint64_t)H};
+  const uint64_t st[3] = {1, (uint64_t)r.row_stride, (uint64_t)r.head_stride};
+  const uint32_t box[3] = {64, (uint32_t)box_rows, 1};
+  return map16(m, r.data, bf16, 3, dims, st, box);
+}
+
+// rows of a group of heads, token by token: (column, head of the group, row, key head)
+inline pisa_status map_query(CUtensorMap *m, const pisa_rows &r, bool bf16, int d, int G, int T, int Hkv,
+                             int tokens) {
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)G, (uint64_t)T, (uint64_t)Hkv};
+  const uint64_t st[4] = {1, (uint64_t)r.head_stride, (uint64_t)r.row_stride, (uint64_t)r.head_stride * G};
+  const uint32_t box[4] = {64, (uint32_t)G, (uint32_t)tokens, 1};
+  return map16(m, r.data, bf16, 4, dims, st, box);
+}
+
+// rows of a page: (column, row, head, page)
+inline pisa_status map_pages(CUtensorMap *m, const pisa_pages &c, bool bf16, int d, int page_size, int H,
+                             int pages) {
+  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)page_size, (uint64_t)H, (uint64_t)pages};
+  const uint64_t st[4] = {1, (uint64_t)c.row_stride, (uint64_t)c.head_stride, (uint64_t)c.page_stride};
+  const uint32_t box[4] = {64, (uint32_t)(page_size < 128 ? page_size : 128), 1, 1};
+  return map16(m, c.data, bf16, 4, dims, st, box);
+}
+
+}  // namespace pisa

@@ -1,0 +1,30 @@
+// sm_100a primitives of the packed and paged kernels beyond sm100_primitives.cuh.
+#pragma once
+
+#include "sm100_primitives.cuh"
+
+namespace pisa {
+namespace sm100 {
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// generic-proxy writes to shared memory, made visible to the tensor cores and TMA
+__device__ __forceinline__ void fence_proxy_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// kind::f16 instruction descriptor with f16 or bf16 A and B, f32 accumulator
+template <bool kBf16> __host__ __device__ constexpr uint32_t idesc_16_f32(int M, int N, int a_mn, int b_mn) {
+  return kBf16 ? idesc_bf16_f32(M, N, a_mn, b_mn)
+               : idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
+}  // namespace sm100
+}  // namespace pisa

@@ -1,0 +1,373 @@
+// How the kernels of packed rows and paged caches share out their work.
+//
+// A batch is B sequences of new tokens, packed: sequence b holds rows cu[b] ..
+// cu[b+1] - 1 of q, and its tokens are the last n of its kv positions (for
+// packed prompts kv = n).  A unit is (sequence, row tile, key head): tq tokens
+// times the G query heads of the key head, G rows a token, against the key
+// tiles of 128 positions that the tile's last token sees.  All units' key
+// tiles, laid end to end, are cut into as many equal ranges as there are CTAs,
+// so every CTA gets the same number of tiles whatever the lengths are.  Nothing
+// is read on the host: the cut depends on lengths in device memory alone, and
+// the grid on the device alone, so a captured launch serves any lengths.
+// A unit inside one range is written by its CTA.  A unit cut by a range's end
+// leaves float32 partial sums, and combine_kernel joins them in ascending CTA
+// order (no atomics: the same inputs give the same bits).
+#pragma once
+
+#include <math.h>
+
+#include "pisa_common.cuh"
+
+namespace pisa {
+
+constexpr int kKeyTile = 128;   // key positions of a tile
+
+struct PackedProblem {
+  const int32_t *cu;        // [B + 1] first row of each sequence
+  const int32_t *kv_lens;   // [B] key positions, or nullptr: the sequences' own lengths
+  int B, T;                 // sequences, rows of q
+  int Hq, Hkv, G;           // query heads, key heads, Hq / Hkv
+  int causal;
+  int tq;                   // tokens of a row tile
+  int max_kv;               // most key positions a sequence can have (table width x page size)
+  int min_tiles;            // no range is cut shorter than this
+};
+
+struct PackedRequest {
+  int first, n, kv, past;   // first row, tokens, key positions, positions before the first token
+};
+
+// Offsets and lengths are device data: whatever they hold, rows stay inside
+// [0, T) and positions inside [0, max_kv].
+__device__ __forceinline__ PackedRequest packed_request(const PackedProblem &p, int b) {
+  PackedRequest r;
+  const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
+  r.first = min(max(lo, 0), p.T);
+  r.n = max(min(hi, p.T) - r.first, 0);
+  r.kv = r.n;
+  if (p.kv_lens) r.kv = min(max(__ldg(p.kv_lens + b), 0), p.max_kv);
+  r.past = r.kv - r.n;
+  return r;
+}
+
+__device__ __forceinline__ bool packed_request_malformed(const PackedProblem &p, int b) {
+  const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
+  bool bad = lo < 0 || hi < lo || hi > p.T;
+  if (p.kv_lens) {
+    const int kv = __ldg(p.kv_lens + b);
+    bad = bad || kv < 0 || kv > p.max_kv;
+  }
+  return bad;
+}
+
+// sum of floor((a i + b) / m) for i = 0 .. n - 1 (the Euclidean recursion on
+// the lattice points under a line); a, m <= 2^8, b < 2^31, a n < 2^31
+__host__ __device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long s = 0;
+  while (n) {
+    s += (long long)(a / m) * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
+    a %= m;
+    b %= m;
+    const unsigned y = a * n + b;
+    n = y / m;
+    b = y % m;
+    const unsigned t = m;
+    m = a;
+    a = t;
+    if (m == 0) break;
+  }
+  return s;
+}
+
+// What a unit costs, in tiles.  RowCost<KT>: a unit is a row tile of tq tokens,
+// its tiles are the KT-key tiles that the last token sees (at least one: a row
+// without keys is still written).  KeyCost: a unit is a tile of 128 keys of a
+// sequence over itself, its tiles are the 128-token tiles of every query head
+// that see it.  before(..., rt): the tiles of units 0 .. rt - 1 of a key head.
+template <int KT> struct RowCost {
+  static __host__ __device__ int units(const PackedProblem &p, int n) { return n > 0 ? (n - 1) / p.tq + 1 : 0; }
+  static __host__ __device__ int tiles(const PackedProblem &p, int n, int kv, int tq, int rt) {
+    const long long past = kv > n ? kv - n : 0;
+    const long long upto = (long long)(rt + 1) * tq;
+    const long long end = p.causal ? past + (n < upto ? n : upto) : (kv > 1 ? kv : 1);
+    return (int)((end + KT - 1) / KT);
+  }
+  static __host__ __device__ int tiles(const PackedProblem &p, int n, int kv, int rt) {
+    return tiles(p, n, kv, p.tq, rt);
+  }
+  static __host__ __device__ long long before(const PackedProblem &p, int n, int kv, int rt) {
+    const int R = units(p, n);
+    if (rt <= 0 || R == 0) return 0;
+    if (!p.causal) return (long long)rt * tiles(p, n, kv, 0);
+    const int past = kv > n ? kv - n : 0;
+    const int whole = rt < R ? rt : R - 1;   // units of tq tokens
+    long long s = floor_sum((unsigned)whole, KT, (unsigned)p.tq, (unsigned)past + (unsigned)p.tq + KT - 1);
+    if (rt >= R) s += tiles(p, n, kv, R - 1);
+    return s;
+  }
+};
+struct KeyCost {
+  static __host__ __device__ int units(const PackedProblem &, int n) { return (n + kKeyTile - 1) / kKeyTile; }
+  static __host__ __device__ int tiles(const PackedProblem &p, int n, int, int rt) {
+    return p.G * (units(p, n) - (p.causal ? rt : 0));
+  }
+  static __host__ __device__ long long before(const PackedProblem &p, int n, int, int rt) {
+    const long long N = units(p, n);
+    return p.G * (rt * N - (p.causal ? (long long)rt * (rt - 1) / 2 : 0));
+  }
+};
+
+template <class Cost>
+__device__ __forceinline__ long long packed_cost(const PackedProblem &p, const PackedRequest &r) {
+  return (long long)p.Hkv * Cost::before(p, r.n, r.kv, Cost::units(p, r.n));
+}
+
+struct PackedStart {
+  long long total;    // key tiles of the whole problem
+  long long w0, w1;   // this CTA's range
+  long long rem;      // w0's distance from the first tile of sequence b
+  int b, ctas;        // sequence of w0; CTAs that have a range
+};
+
+__host__ __device__ __forceinline__ long long packed_range_start(long long total, int ctas, int c) {
+  return total * c / ctas;
+}
+
+// One call by all `threads` threads of a CTA (a multiple of 32, at most 512):
+// fills *out (shared memory).  Contains two CTA barriers.
+template <class Cost>
+__device__ __forceinline__ void packed_locate(const PackedProblem &p, int cta, int grid, int tid,
+                                              int threads, long long *warp_sum, PackedStart *out) {
+  const int per = (p.B + threads - 1) / threads;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  long long own = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    own += packed_cost<Cost>(p, packed_request(p, b));
+    bad = bad || packed_request_malformed(p, b);
+  }
+  if (bad && cta == 0) report_device_error(kDevErrRange);
+  const int lane = tid & 31, warp = tid >> 5;
+  long long incl = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long before = incl - own, total = 0;
+  for (int w = 0; w < threads / 32; ++w) {
+    const long long s = warp_sum[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  const long long want = total / p.min_tiles;
+  const int ctas = want < 1 ? 1 : want < grid ? (int)want : grid;
+  const long long w0 = cta < ctas ? packed_range_start(total, ctas, cta) : total;
+  const long long w1 = cta < ctas ? packed_range_start(total, ctas, cta + 1) : total;
+  if (tid == 0 && w0 >= total) {
+    out->total = total;
+    out->w0 = out->w1 = total;
+    out->rem = 0;
+    out->b = p.B;
+    out->ctas = ctas;
+  }
+  if (own > 0 && w0 >= before && w0 < before + own) {
+    long long rem = w0 - before;
+    int b = b0;
+    for (;; ++b) {
+      const long long c = packed_cost<Cost>(p, packed_request(p, b));
+      if (rem < c) break;
+      rem -= c;
+    }
+    out->total = total;
+    out->w0 = w0;
+    out->w1 = w1;
+    out->rem = rem;
+    out->b = b;
+    out->ctas = ctas;
+  }
+  __syncthreads();
+}
+
+// The part [ta, tb) of one unit's key tiles [0, nt)
+struct PackedSegment {
+  PackedRequest r;
+  int b, rt, h, nt, ta, tb;
+  __device__ __forceinline__ bool whole() const { return ta == 0 && tb == nt; }
+  // partial slot of the CTA: 0 holds a unit begun by an earlier CTA, 1 one that goes on in the next
+  __device__ __forceinline__ int slot() const { return ta != 0 ? 0 : 1; }
+};
+
+// Walks a CTA's range segment by segment.  Every warp keeps its own (all lanes
+// hold the same values), so no role waits for another to learn what comes next.
+template <class Cost> struct PackedWalk {
+  PackedSegment s;
+  long long left;
+  int t;         // first tile of the next segment inside its unit
+  // all 32 lanes of a converged warp
+  __device__ __forceinline__ void begin(const PackedProblem &p, const PackedStart &st) {
+    left = st.w1 - st.w0;
+    t = 0;
+    s.b = st.b;
+    s.rt = 0;
+    s.h = 0;
+    if (left <= 0) return;
+    s.r = packed_request(p, s.b);
+    // last row tile whose first key tile is at or before rem: 32-way search
+    int lo = 0, hi = Cost::units(p, s.r.n);   // answer in [lo, hi)
+    const int lane = threadIdx.x & 31;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const bool ok = at < hi && p.Hkv * Cost::before(p, s.r.n, s.r.kv, at) <= st.rem;
+      const unsigned m = __ballot_sync(0xffffffffu, ok);   // lane 0 always holds
+      const int last = 31 - __clz(m);
+      lo += last * step;
+      hi = min(hi, lo + step);
+    }
+    s.rt = lo;
+    s.nt = Cost::tiles(p, s.r.n, s.r.kv, lo);
+    const long long in = st.rem - p.Hkv * Cost::before(p, s.r.n, s.r.kv, lo);
+    s.h = (int)(in / s.nt);
+    t = (int)(in % s.nt);
+  }
+  __device__ __forceinline__ bool next(const PackedProblem &p) {
+    if (left <= 0) return false;
+    if (t == kDone) {
+      t = 0;
+      if (++s.h == p.Hkv) {
+        s.h = 0;
+        if (++s.rt >= Cost::units(p, s.r.n)) {
+          s.rt = 0;
+          do {
+            if (++s.b >= p.B) return false;   // cannot happen while tiles are left
+            s.r = packed_request(p, s.b);
+          } while (s.r.n == 0);
+        }
+        s.nt = Cost::tiles(p, s.r.n, s.r.kv, s.rt);
+      }
+    }
+    s.ta = t;
+    s.tb = (int)(left < s.nt - t ? t + left : s.nt);
+    left -= s.tb - s.ta;
+    t = s.tb == s.nt ? kDone : s.tb;
+    return true;
+  }
+  static constexpr int kDone = -1;
+};
+
+// What a CTA says about the unit that its range's end cuts (slot 1)
+struct PackedCut {
+  int valid, b, rt, h, last;   // last: the CTA that holds the unit's last tile
+};
+
+__device__ __forceinline__ PackedCut packed_cut(const PackedStart &st, const PackedSegment &s) {
+  PackedCut c;
+  c.valid = 1;
+  c.b = s.b;
+  c.rt = s.rt;
+  c.h = s.h;
+  const long long end = st.w1 + (s.nt - s.tb) - 1;   // the unit's last tile
+  c.last = (int)(((end + 1) * st.ctas - 1) / st.total);
+  return c;
+}
+
+// partial slot: R rows of m and l, then the unnormalised output as [D / 4][R] float4
+template <int D> __host__ __device__ constexpr size_t packed_slot_floats(int R) {
+  return (size_t)R * (D + 2);
+}
+
+template <typename T> struct Half16;
+template <> struct Half16<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+  static __device__ __forceinline__ float2 unpack(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+  }
+};
+template <> struct Half16<__half> {
+  static constexpr bool kBf16 = false;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t x) {
+    return __half22float2(*reinterpret_cast<__half2 *>(&x));
+  }
+};
+
+struct PackedOut {
+  void *out;                // 16-bit rows
+  long long head, row;      // strides in elements
+  float *lse;               // [Hq, T] or nullptr
+  float *f32;               // [Hq, T, D] or nullptr
+};
+
+// Zeros rows [cu[B], T) of a 16-bit tensor of H heads: rows that belong to no
+// sequence.  All threads of a grid of `threads` threads, this one the `me`-th.
+template <int D>
+__device__ __forceinline__ void clear_tail(const PackedProblem &p, int H, void *out, long long head_stride,
+                                           long long row_stride, long long me, long long threads) {
+  const int end = min(max(__ldg(p.cu + p.B), 0), p.T);
+  const long long n = (long long)H * (p.T - end) * (D / 8);
+  for (long long e = me; e < n; e += threads) {
+    const long long r = e / (D / 8);
+    const int h = (int)(r / (p.T - end)), t = end + (int)(r % (p.T - end));
+    reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + h * head_stride + t * row_stride)[e % (D / 8)] =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Joins the partials of the unit that CTA blockIdx.x's range cuts:
+//   m = max_i m_i,  l = sum_i l_i 2^(m_i - m),  o = sum_i O_i 2^(m_i - m) / l
+// (m in units of log2).  One thread per (row, four columns).
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+    packed_combine_kernel(const PackedProblem p, const PackedCut *__restrict__ cuts,
+                          const float *__restrict__ part, int R, const PackedOut o, int clear) {
+  if (clear)
+    clear_tail<D>(p, p.Hq, o.out, o.head, o.row,
+                  ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                  (long long)gridDim.x * gridDim.y * blockDim.x);
+  const PackedCut cut = cuts[blockIdx.x];
+  if (!cut.valid) return;
+  const PackedRequest r = packed_request(p, cut.b);
+  const int tok0 = cut.rt * p.tq, rows = min(r.n - tok0, p.tq) * p.G;
+  const size_t slot = packed_slot_floats<D>(R);
+  const int c0 = blockIdx.x, n = cut.last - c0 + 1;
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 4); e += gridDim.y * blockDim.x) {
+    const int row = e / (D / 4), c4 = e % (D / 4);
+    // partial i: slot 1 of the first CTA, slot 0 of the later ones
+    auto at = [&](int i) { return part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot; };
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[row]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; ++i) {
+      const float *s = at(i);
+      const float f = exp2f(s[row] - base);
+      if (f == 0.f) continue;   // no weight (and, of a tile without keys, no output either)
+      const float4 x = reinterpret_cast<const float4 *>(s + 2 * R)[(size_t)c4 * R + row];
+      l = fmaf(f, s[R + row], l);
+      acc.x = fmaf(f, x.x, acc.x);
+      acc.y = fmaf(f, x.y, acc.y);
+      acc.z = fmaf(f, x.z, acc.z);
+      acc.w = fmaf(f, x.w, acc.w);
+    }
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // a row without keys is zero; NaN stays
+    const int token = r.first + tok0 + row / p.G, head = cut.h * p.G + row % p.G;
+    uint2 w;
+    w.x = Half16<T>::pack(acc.x * inv, acc.y * inv);
+    w.y = Half16<T>::pack(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2 *>(reinterpret_cast<T *>(o.out) + head * o.head + token * o.row + 4 * c4) = w;
+    const size_t hr = (size_t)head * p.T + token;
+    if (o.f32)
+      reinterpret_cast<float4 *>(o.f32 + hr * D)[c4] =
+          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (o.lse && c4 == 0) o.lse[hr] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+}  // namespace pisa

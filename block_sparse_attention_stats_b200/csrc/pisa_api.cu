@@ -1,5 +1,5 @@
-// libpisa C ABI: argument checking, scratch layout and kernel launches.
-// One translation unit: every kernel header is included here.
+// libpisa C ABI: argument checking, scratch layout and kernel launches of the
+// piecewise sparse path.  (Packed sequences and the paged cache: pisa_packed.cu.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -30,6 +30,8 @@ static thread_local std::string t_last_error;
 void set_last_error(cudaError_t e) {
   t_last_error = std::string(cudaGetErrorName(e)) + ": " + cudaGetErrorString(e);
 }
+
+void set_last_error_text(const std::string &text) { t_last_error = text; }
 
 pisa_status check_launch() {
   cudaError_t e = cudaGetLastError();
@@ -319,7 +321,7 @@ static pisa_status launch_select(const float *qbar, const float *kbar, const flo
 // ---- tensor maps for the tensor-memory-accelerator loads ------------------------
 using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
 
-static EncodeTiledFn encode_tiled() {
+EncodeTiledFn encode_tiled() {
   static EncodeTiledFn fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -1184,19 +1186,9 @@ pisa_status pisa_device_status(pisa_stream_t stream) {
     return PISA_ERR_CUDA;
   }
   unsigned v = 0;
-  e = cudaMemcpyFromSymbol(&v, g_device_status, sizeof(v));
-  if (e != cudaSuccess) {
-    set_last_error(e);
-    return PISA_ERR_CUDA;
-  }
-  if (v) {
-    const unsigned zero = 0;
-    e = cudaMemcpyToSymbol(g_device_status, &zero, sizeof(zero));
-    if (e != cudaSuccess) {
-      set_last_error(e);
-      return PISA_ERR_CUDA;
-    }
-  }
+  PISA_TRY(take_status_word(&g_device_status, &v));
+  PISA_TRY(take_packed_status(&v));
+  PISA_TRY(take_packed_bwd_status(&v));
   if (v & kDevErrTimeout) return PISA_ERR_TIMEOUT;
   if (v & kDevErrRange) return PISA_ERR_DEVICE;
   return PISA_OK;

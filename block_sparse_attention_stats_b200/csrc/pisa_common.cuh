@@ -1,11 +1,17 @@
-// Shared device helpers of libpisa (sm_100a).  libpisa is one translation
-// unit: pisa_api.cu includes every kernel header, so no relocatable device
-// code is needed.
+// Shared device helpers of libpisa (sm_100a).  Each translation unit
+// (pisa_api.cu, pisa_packed.cu, pisa_packed_bwd.cu) includes the kernel headers it launches, so no
+// relocatable device code is needed; each has its own device status word, and
+// pisa_device_status reads them all.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <string>
 
 #include "pisa.h"
 
@@ -15,7 +21,7 @@ namespace pisa {
 // device status word: bit 0 = range check failed, bit 1 = bounded wait ran out
 // ---------------------------------------------------------------------------
 enum : unsigned { kDevErrRange = 1u, kDevErrTimeout = 2u };
-__device__ unsigned g_device_status;
+static __device__ unsigned g_device_status;
 
 __device__ __forceinline__ void report_device_error(unsigned bits) {
   atomicOr(&g_device_status, bits);
@@ -102,6 +108,26 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], const uint32_t (&a
 // host-side helpers
 // ---------------------------------------------------------------------------
 void set_last_error(cudaError_t e);
+void set_last_error_text(const std::string &text);
 pisa_status check_launch();
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled();   // nullptr where the driver lacks it
+
+// Reads and clears one translation unit's device status word (the current device's).
+template <typename Word> pisa_status take_status_word(Word *symbol, unsigned *bits) {
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, *symbol, sizeof(v));
+  if (e == cudaSuccess && v) {
+    const unsigned zero = 0;
+    e = cudaMemcpyToSymbol(*symbol, &zero, sizeof(zero));
+  }
+  if (e != cudaSuccess) {
+    set_last_error(e);
+    return PISA_ERR_CUDA;
+  }
+  *bits |= v;
+  return PISA_OK;
+}
+pisa_status take_packed_status(unsigned *bits);       // pisa_packed.cu's
+pisa_status take_packed_bwd_status(unsigned *bits);   // pisa_packed_bwd.cu's
 
 }  // namespace pisa

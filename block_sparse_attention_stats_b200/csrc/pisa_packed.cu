@@ -1,0 +1,350 @@
+// libpisa C ABI, second translation unit: attention over packed sequences and
+// over a paged key/value cache, with the cache's bookkeeping.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "packed_host.cuh"
+#include "packed_schedule.cuh"
+#include "k9_pages.cuh"
+#include "k10_attend_rows.cuh"
+#include "k11_attend_tc.cuh"
+
+namespace pisa {
+
+pisa_status take_packed_status(unsigned *bits) { return take_status_word(&g_device_status, bits); }
+
+// ---- scratch ---------------------------------------------------------------------
+// Two partial slots and one cut a CTA (rows: of a unit).
+struct PackedScratch {
+  size_t cuts, part, total;
+};
+static PackedScratch packed_scratch(int d, int rows) {
+  PackedScratch s;
+  s.cuts = 0;
+  s.part = align_up(kPackedCtas * sizeof(PackedCut), 256);
+  s.total = s.part + align_up((size_t)kPackedCtas * 2 * rows * (d + 2) * sizeof(float), 256);
+  return s;
+}
+
+// ---- launches ----------------------------------------------------------------------
+template <typename T, int D>
+static pisa_status launch_combine(const PackedProblem &p, const PackedCut *cuts, const float *part, int R,
+                                  const PackedOut &o, int clear, cudaStream_t st) {
+  // a few hundred rows by D / 4 threads each are joined per cut unit
+  const int y = std::max(1, std::min(16, R * (D / 4) / 256));
+  packed_combine_kernel<T, D><<<dim3(kPackedCtas, y), 256, 0, st>>>(p, cuts, part, R, o, clear);
+  return check_launch();
+}
+
+template <typename T, int D, bool PAGED>
+static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_rows &q, const CUtensorMap &mk,
+                             const CUtensorMap &mv, float scale, const PackedOut &o, int clear,
+                             unsigned char *ws, cudaStream_t st) {
+  using C = AttendCfg<D>;
+  const int tq1 = 128 / p.G;
+  p.tq = 2 * tq1;
+  p.min_tiles = 2;
+  CUtensorMap mq;
+  PISA_TRY(map_query(&mq, q, Half16<T>::kBf16, D, p.G, p.T, p.Hkv, tq1));
+  const PackedScratch s = packed_scratch(D, C::kRows);
+  PackedCut *cuts = (PackedCut *)(ws + s.cuts);
+  float *part = (float *)(ws + s.part);
+  PISA_CUDA(cudaFuncSetAttribute(attend_tc_kernel<T, D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem));
+  attend_tc_kernel<T, D, PAGED><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(mq, mk, mv, p, cache, scale, o,
+                                                                            cuts, part);
+  PISA_TRY(check_launch());
+  return launch_combine<T, D>(p, cuts, part, C::kRows, o, clear, st);
+}
+
+template <typename T, int D, int R>
+static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa_rows &q, const CUtensorMap &mk,
+                               const CUtensorMap &mv, float scale, const PackedOut &o, unsigned char *ws,
+                               cudaStream_t st) {
+  using C = RowsCfg<D, R>;
+  p.tq = R / p.G;
+  p.min_tiles = 1;
+  const PackedScratch s = packed_scratch(D, R);
+  PackedCut *cuts = (PackedCut *)(ws + s.cuts);
+  float *part = (float *)(ws + s.part);
+  PISA_CUDA(cudaFuncSetAttribute(attend_rows_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem));
+  attend_rows_kernel<T, D, R><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(
+      mk, mv, p, cache, (const T *)q.data, q.head_stride, q.row_stride, scale, o, cuts, part);
+  PISA_TRY(check_launch());
+  return launch_combine<T, D>(p, cuts, part, R, o, 0, st);
+}
+
+template <typename T, int D>
+static pisa_status run_varlen(const PackedProblem &p, const pisa_rows &q, const pisa_rows &k,
+                              const pisa_rows &v, float scale, const PackedOut &o, int clear,
+                              unsigned char *ws, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  PISA_TRY(map_rows(&mk, k, Half16<T>::kBf16, D, p.T, p.Hkv, kKeyTile));
+  PISA_TRY(map_rows(&mv, v, Half16<T>::kBf16, D, p.T, p.Hkv, kKeyTile));
+  return launch_tc<T, D, false>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
+}
+
+template <typename T, int D>
+static pisa_status run_paged(const PackedProblem &p, const PagedKV &cache, const pisa_rows &q,
+                             const pisa_pages &k, const pisa_pages &v, float scale, const PackedOut &o,
+                             unsigned char *ws, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  PISA_TRY(map_pages(&mk, k, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages));
+  PISA_TRY(map_pages(&mv, v, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages));
+  // rows of an average request (the lengths themselves are on the device; either kernel
+  // serves any of them).
+  const long long rows = ((long long)p.T * p.G + p.B - 1) / p.B;
+  const long long r = std::max<long long>(rows, p.G);
+  if (r <= 16) return launch_rows<T, D, 16>(p, cache, q, mk, mv, scale, o, ws, st);
+  if (r <= 32) return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
+  if (r <= 64) return launch_rows<T, D, 64>(p, cache, q, mk, mv, scale, o, ws, st);
+  return launch_tc<T, D, true>(p, cache, q, mk, mv, scale, o, 0, ws, st);
+}
+
+// ---- argument checks --------------------------------------------------------------------
+static pisa_status check_heads(int B, int T, int Hq, int Hkv, int d, pisa_dtype dtype) {
+  if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv) return PISA_ERR_INVALID_ARG;
+  if (dtype != PISA_BF16 && dtype != PISA_F16 && dtype != PISA_F32) return PISA_ERR_INVALID_ARG;
+  if (dtype == PISA_F32) return PISA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return PISA_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hq / Hkv > 128 || T > (1 << 24) || B > (1 << 24)) return PISA_ERR_UNSUPPORTED;
+  return PISA_OK;
+}
+
+static PackedProblem problem(const int32_t *cu, const int32_t *kv_lens, int B, int T, int Hq, int Hkv,
+                             int causal, long long max_kv) {
+  PackedProblem p{};
+  p.cu = cu;
+  p.kv_lens = kv_lens;
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.causal = causal != 0;
+  p.max_kv = (int)std::min<long long>(max_kv, 0x7fffff00ll);
+  return p;
+}
+
+static bool is_int32(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
+
+static pisa_status check_pages(const pisa_pages &c, int H, int ps, int pages, int d) {
+  if (!aligned16(c.data)) return PISA_ERR_INVALID_ARG;
+  const int64_t s[3] = {c.page_stride, c.head_stride, c.row_stride};
+  const int n[3] = {pages, H, ps};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] < d || s[i] % 8 || s[i] >= (1ll << 38))) return PISA_ERR_INVALID_ARG;
+  return PISA_OK;
+}
+
+static bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
+
+static pisa_status check_step(const pisa_page_step *s) {
+  if (!s || s->B < 1 || s->T < 0 || s->width < 1 || s->page_size < 1 || s->free_cap < 0)
+    return PISA_ERR_INVALID_ARG;
+  if (!page_size_ok(s->page_size) || s->B > kPlanMaxB || s->T > (1 << 24)) return PISA_ERR_UNSUPPORTED;
+  if ((long long)s->width * s->page_size > 0x7fffffffll) return PISA_ERR_UNSUPPORTED;
+  if (!is_int32(s->past_lens) || !is_int32(s->new_lens) || !is_int32(s->block_table) ||
+      !is_int32(s->num_free) || !is_int32(s->cu_seqlens) || !is_int32(s->kv_lens) ||
+      !is_int32(s->num_free_out))
+    return PISA_ERR_INVALID_ARG;
+  if (s->free_cap && !is_int32(s->free_pages)) return PISA_ERR_INVALID_ARG;
+  if (s->T && (!s->slots || ((uintptr_t)s->slots & 7u))) return PISA_ERR_INVALID_ARG;
+  // every CTA reads the lengths, the free list and its count while others write
+  const void *in[] = {s->past_lens, s->new_lens, s->num_free, s->free_pages};
+  const void *out[] = {s->cu_seqlens, s->kv_lens, s->num_free_out, s->block_table, s->slots};
+  for (const void *o : out)
+    for (const void *i : in)
+      if (o && o == i) return PISA_ERR_INVALID_ARG;
+  for (int a = 0; a < 5; ++a)
+    for (int b = 0; b < a; ++b)
+      if (out[a] && out[a] == out[b]) return PISA_ERR_INVALID_ARG;
+  return PISA_OK;
+}
+
+}  // namespace pisa
+
+using namespace pisa;
+
+extern "C" {
+
+size_t pisa_varlen_attention_workspace_bytes(int Hq, int Hkv, int d) {
+  if (check_heads(1, 1, Hq, Hkv, d, PISA_BF16) != PISA_OK) return 0;
+  return packed_scratch(d, 256).total;
+}
+
+pisa_status pisa_varlen_attention(pisa_rows q, pisa_rows k, pisa_rows v, pisa_dtype dtype,
+                                  const int32_t *cu_seqlens, int B, int T, int Hq, int Hkv, int d,
+                                  float scale, int flags, pisa_rows out, float *lse, float *out_f32,
+                                  void *workspace, size_t ws_bytes, pisa_stream_t stream) {
+  PISA_TRY(check_heads(B, T, Hq, Hkv, d, dtype));
+  if (!(scale >= 0.f) || !std::isfinite(scale) || !is_int32(cu_seqlens)) return PISA_ERR_INVALID_ARG;
+  if (flags & ~(PISA_CAUSAL | PISA_ZERO_TAIL)) return PISA_ERR_INVALID_ARG;
+  if (T == 0) return PISA_OK;
+  PISA_TRY(check_rows(q, Hq, T, d, false));
+  PISA_TRY(check_rows(k, Hkv, T, d, false));
+  PISA_TRY(check_rows(v, Hkv, T, d, false));
+  PISA_TRY(check_rows(out, Hq, T, d, true));
+  if (out.data == q.data || out.data == k.data || out.data == v.data) return PISA_ERR_INVALID_ARG;
+  if (lse && !is_int32(lse)) return PISA_ERR_INVALID_ARG;
+  if (out_f32 && (!aligned16(out_f32) || (void *)out_f32 == out.data)) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
+  if (ws_bytes < packed_scratch(d, 256).total) return PISA_ERR_WORKSPACE;
+  const PackedProblem p = problem(cu_seqlens, nullptr, B, T, Hq, Hkv, flags & PISA_CAUSAL, T);
+  const PackedOut o{out.data, out.head_stride, out.row_stride, lse, out_f32};
+  const int clear = flags & PISA_ZERO_TAIL;
+  const float s = scale == 0.f ? 1.f / std::sqrt((float)d) : scale;
+  unsigned char *ws = (unsigned char *)workspace;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == PISA_BF16)
+    return d == 128 ? run_varlen<__nv_bfloat16, 128>(p, q, k, v, s, o, clear, ws, st)
+                    : run_varlen<__nv_bfloat16, 64>(p, q, k, v, s, o, clear, ws, st);
+  return d == 128 ? run_varlen<__half, 128>(p, q, k, v, s, o, clear, ws, st)
+                  : run_varlen<__half, 64>(p, q, k, v, s, o, clear, ws, st);
+}
+
+size_t pisa_paged_attention_workspace_bytes(int Hq, int Hkv, int d) {
+  return pisa_varlen_attention_workspace_bytes(Hq, Hkv, d);
+}
+
+pisa_status pisa_paged_attention(pisa_rows q, pisa_pages k_cache, pisa_pages v_cache, pisa_dtype dtype,
+                                 int num_pages, int page_size, const int32_t *block_table, int width,
+                                 const int32_t *cu_seqlens, const int32_t *kv_lens, int B, int T, int Hq,
+                                 int Hkv, int d, float scale, pisa_rows out, float *lse, void *workspace,
+                                 size_t ws_bytes, pisa_stream_t stream) {
+  PISA_TRY(check_heads(B, T, Hq, Hkv, d, dtype));
+  if (num_pages < 1 || page_size < 1 || width < 1) return PISA_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size)) return PISA_ERR_UNSUPPORTED;
+  if (!(scale >= 0.f) || !std::isfinite(scale)) return PISA_ERR_INVALID_ARG;
+  if (!is_int32(block_table) || !is_int32(cu_seqlens) || !is_int32(kv_lens)) return PISA_ERR_INVALID_ARG;
+  if (T == 0) return PISA_OK;
+  PISA_TRY(check_rows(q, Hq, T, d, false));
+  PISA_TRY(check_rows(out, Hq, T, d, true));
+  PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d));
+  PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d));
+  if (out.data == q.data || out.data == k_cache.data || out.data == v_cache.data) return PISA_ERR_INVALID_ARG;
+  if (lse && !is_int32(lse)) return PISA_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
+  if (ws_bytes < packed_scratch(d, 256).total) return PISA_ERR_WORKSPACE;
+  const PackedProblem p = problem(cu_seqlens, kv_lens, B, T, Hq, Hkv, 1, (long long)width * page_size);
+  const PagedKV cache{block_table, width, page_size, num_pages};
+  const PackedOut o{out.data, out.head_stride, out.row_stride, lse, nullptr};
+  const float s = scale == 0.f ? 1.f / std::sqrt((float)d) : scale;
+  unsigned char *ws = (unsigned char *)workspace;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == PISA_BF16)
+    return d == 128 ? run_paged<__nv_bfloat16, 128>(p, cache, q, k_cache, v_cache, s, o, ws, st)
+                    : run_paged<__nv_bfloat16, 64>(p, cache, q, k_cache, v_cache, s, o, ws, st);
+  return d == 128 ? run_paged<__half, 128>(p, cache, q, k_cache, v_cache, s, o, ws, st)
+                  : run_paged<__half, 64>(p, cache, q, k_cache, v_cache, s, o, ws, st);
+}
+
+pisa_status pisa_page_plan(const pisa_page_step *step, pisa_stream_t stream) {
+  PISA_TRY(check_step(step));
+  PagePlan p{};
+  p.past = step->past_lens;
+  p.fresh = step->new_lens;
+  p.B = step->B;
+  p.T = step->T;
+  p.width = step->width;
+  p.page_size = step->page_size;
+  p.table = step->block_table;
+  p.free_pages = step->free_pages;
+  p.free_cap = step->free_cap;
+  p.num_free = step->num_free;
+  p.slots = step->slots;
+  p.cu = step->cu_seqlens;
+  p.kv_lens = step->kv_lens;
+  p.num_free_out = step->num_free_out;
+  const int smem = 2 * (p.B + 1) * (int)sizeof(int);
+  PISA_CUDA(cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 2 * (kPlanMaxB + 1) * (int)sizeof(int)));
+  const int work = std::max(p.T, p.B + 1);
+  const int grid = std::max(1, std::min(ceil_div(work, kPlanThreads), kPackedCtas));
+  page_plan_kernel<<<grid, kPlanThreads, smem, (cudaStream_t)stream>>>(p);
+  return check_launch();
+}
+
+pisa_status pisa_page_write(pisa_rows k, pisa_rows v, pisa_dtype dtype, const int64_t *slots, int T, int Hkv,
+                            int d, pisa_pages k_cache, pisa_pages v_cache, int num_pages, int page_size,
+                            pisa_stream_t stream) {
+  PISA_TRY(check_heads(1, T, Hkv, Hkv, d, dtype));
+  if (num_pages < 1 || page_size < 1) return PISA_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size)) return PISA_ERR_UNSUPPORTED;
+  if (T == 0) return PISA_OK;
+  if (!slots || ((uintptr_t)slots & 7u)) return PISA_ERR_INVALID_ARG;
+  PISA_TRY(check_rows(k, Hkv, T, d, false));
+  PISA_TRY(check_rows(v, Hkv, T, d, false));
+  PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d));
+  PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d));
+  const void *src[2] = {k.data, v.data}, *dst[2] = {k_cache.data, v_cache.data};
+  if (dst[0] == dst[1]) return PISA_ERR_INVALID_ARG;
+  for (const void *a : src)
+    for (const void *b : dst)
+      if (a == b) return PISA_ERR_INVALID_ARG;
+  PageWrite w{};
+  const pisa_rows r[2] = {k, v};
+  const pisa_pages c[2] = {k_cache, v_cache};
+  for (int i = 0; i < 2; ++i) {
+    w.src[i] = (const unsigned char *)r[i].data;
+    w.src_head[i] = r[i].head_stride * 2;
+    w.src_row[i] = r[i].row_stride * 2;
+    w.dst[i] = (unsigned char *)c[i].data;
+    w.dst_page[i] = c[i].page_stride * 2;
+    w.dst_head[i] = c[i].head_stride * 2;
+    w.dst_row[i] = c[i].row_stride * 2;
+  }
+  w.slots = slots;
+  w.T = T;
+  w.H = Hkv;
+  w.page_size = page_size;
+  w.num_slots = (long long)num_pages * page_size;
+  const int per = kWriteThreads / (d / 8) * kWriteRows;
+  const dim3 grid(std::min(ceil_div(T, per), 65535), Hkv, 2);
+  if (d == 128)
+    page_write_kernel<16><<<grid, kWriteThreads, 0, (cudaStream_t)stream>>>(w);
+  else
+    page_write_kernel<8><<<grid, kWriteThreads, 0, (cudaStream_t)stream>>>(w);
+  return check_launch();
+}
+
+pisa_status pisa_paged_step(const pisa_page_step *step, pisa_rows q, pisa_rows k, pisa_rows v,
+                            pisa_pages k_cache, pisa_pages v_cache, pisa_dtype dtype, int num_pages, int Hq,
+                            int Hkv, int d, float scale, pisa_rows out, float *lse, void *workspace,
+                            size_t ws_bytes, pisa_stream_t stream) {
+  PISA_TRY(check_step(step));
+  // everything is checked before the plan changes the table
+  const int B = step->B, T = step->T, ps = step->page_size;
+  PISA_TRY(check_heads(B, T, Hq, Hkv, d, dtype));
+  if (num_pages < 1 || !(scale >= 0.f) || !std::isfinite(scale)) return PISA_ERR_INVALID_ARG;
+  if (lse && !is_int32(lse)) return PISA_ERR_INVALID_ARG;
+  if (T) {
+    PISA_TRY(check_rows(q, Hq, T, d, false));
+    PISA_TRY(check_rows(k, Hkv, T, d, false));
+    PISA_TRY(check_rows(v, Hkv, T, d, false));
+    PISA_TRY(check_rows(out, Hq, T, d, true));
+    PISA_TRY(check_pages(k_cache, Hkv, ps, num_pages, d));
+    PISA_TRY(check_pages(v_cache, Hkv, ps, num_pages, d));
+    const void *src[3] = {q.data, k.data, v.data}, *dst[3] = {k_cache.data, v_cache.data, out.data};
+    for (const void *a : src)
+      for (const void *b : dst)
+        if (a == b) return PISA_ERR_INVALID_ARG;
+    if (dst[0] == dst[1] || dst[0] == dst[2] || dst[1] == dst[2]) return PISA_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
+    if (ws_bytes < packed_scratch(d, 256).total) return PISA_ERR_WORKSPACE;
+  }
+  PISA_TRY(pisa_page_plan(step, stream));
+  PISA_TRY(pisa_page_write(k, v, dtype, step->slots, T, Hkv, d, k_cache, v_cache, num_pages, ps, stream));
+  return pisa_paged_attention(q, k_cache, v_cache, dtype, num_pages, ps, step->block_table, step->width,
+                              step->cu_seqlens, step->kv_lens, B, T, Hq, Hkv, d, scale, out, lse, workspace,
+                              ws_bytes, stream);
+}
+
+}  // extern "C"

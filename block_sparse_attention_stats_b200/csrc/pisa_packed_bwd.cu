@@ -1,0 +1,135 @@
+// libpisa C ABI, third translation unit: gradients of attention over packed
+// sequences.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "packed_host.cuh"
+#include "packed_schedule.cuh"
+#include "k12_packed_bwd.cuh"
+
+namespace pisa {
+
+pisa_status take_packed_bwd_status(unsigned *bits) { return take_status_word(&g_device_status, bits); }
+
+struct PackedBwdLayout {
+  size_t lse2, delta, cuts, part, total;
+};
+static PackedBwdLayout packed_bwd_layout(int T, int Hq, int d) {
+  PackedBwdLayout l;
+  const size_t rows = align_up((size_t)Hq * T * sizeof(float), 256);
+  l.lse2 = 0;
+  l.delta = rows;
+  l.cuts = 2 * rows;
+  l.part = l.cuts + align_up(kPackedCtas * sizeof(PackedCut), 256);
+  // partial sums of dq, then of dk and dv (the two kernels run one after the other)
+  l.total = l.part + (size_t)kPackedCtas * 2 * 2 * 128 * d * sizeof(float);
+  return l;
+}
+
+template <int D>
+static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const pisa_rows &k, const pisa_rows &v,
+                                     const pisa_rows &dout, const float *lse, const float *out_f32, float scale,
+                                     const pisa_rows &dq, const pisa_rows &dk, const pisa_rows &dv,
+                                     int clear, unsigned char *ws, cudaStream_t st) {
+  using C = PackedBwdCfg<D>;
+  const PackedBwdLayout l = packed_bwd_layout(p.T, p.Hq, D);
+  float *lse2 = (float *)(ws + l.lse2), *delta = (float *)(ws + l.delta), *part = (float *)(ws + l.part);
+  PackedCut *cuts = (PackedCut *)(ws + l.cuts);
+  const long long rows = (long long)p.Hq * p.T;
+  packed_delta_kernel<D><<<(unsigned)std::min<long long>((rows + 7) / 8, 148 * 8), 256, 0, st>>>(
+      (const __nv_bfloat16 *)dout.data, dout.head_stride, dout.row_stride, out_f32, lse, p.Hq, p.T, p.cu, p.B,
+      lse2, delta);
+  PISA_TRY(check_launch());
+  p.tq = 128 / p.G;
+  p.min_tiles = 2;
+  CUtensorMap mq, mdo, mk, mv;
+  PISA_TRY(map_query(&mq, q, true, D, p.G, p.T, p.Hkv, p.tq));
+  PISA_TRY(map_query(&mdo, dout, true, D, p.G, p.T, p.Hkv, p.tq));
+  PISA_TRY(map_rows(&mk, k, true, D, p.T, p.Hkv, 128));
+  PISA_TRY(map_rows(&mv, v, true, D, p.T, p.Hkv, 128));
+  PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem));
+  packed_bwd_kernel<D, false><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(
+      mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr,
+      0, 0, cuts, part);
+  PISA_TRY(check_launch());
+  packed_sum_kernel<D, false><<<dim3(kPackedCtas, 8), 256, 0, st>>>(
+      p, cuts, part, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr, 0, 0, clear);
+  PISA_TRY(check_launch());
+  // dk, dv: Q and dout one head at a time
+  PISA_TRY(map_rows(&mq, q, true, D, p.T, p.Hq, 128));
+  PISA_TRY(map_rows(&mdo, dout, true, D, p.T, p.Hq, 128));
+  PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmemKv));
+  packed_bwd_kernel<D, true><<<kPackedCtas, C::kThreads, C::kSmemKv, st>>>(
+      mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dk.data, dk.head_stride, dk.row_stride,
+      (__nv_bfloat16 *)dv.data, dv.head_stride, dv.row_stride, cuts, part);
+  PISA_TRY(check_launch());
+  packed_sum_kernel<D, true><<<dim3(kPackedCtas, 8, 2), 256, 0, st>>>(
+      p, cuts, part, (__nv_bfloat16 *)dk.data, dk.head_stride, dk.row_stride, (__nv_bfloat16 *)dv.data,
+      dv.head_stride, dv.row_stride, clear);
+  return check_launch();
+}
+
+}  // namespace pisa
+
+using namespace pisa;
+
+extern "C" {
+
+size_t pisa_varlen_attention_bwd_workspace_bytes(int T, int Hq, int Hkv, int d) {
+  if (T < 1 || T > (1 << 24) || pisa_varlen_attention_workspace_bytes(Hq, Hkv, d) == 0) return 0;
+  return packed_bwd_layout(T, Hq, d).total;
+}
+
+pisa_status pisa_varlen_attention_bwd(pisa_rows q, pisa_rows k, pisa_rows v, pisa_rows dout, pisa_dtype dtype,
+                                      const float *lse, const float *out_f32, const int32_t *cu_seqlens, int B,
+                                      int T, int Hq, int Hkv, int d, float scale, int flags, pisa_rows dq,
+                                      pisa_rows dk, pisa_rows dv, void *workspace, size_t ws_bytes,
+                                      pisa_stream_t stream) {
+  if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv) return PISA_ERR_INVALID_ARG;
+  if (dtype != PISA_BF16 && dtype != PISA_F16 && dtype != PISA_F32) return PISA_ERR_INVALID_ARG;
+  if (dtype != PISA_BF16 || (d != 64 && d != 128)) return PISA_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hq / Hkv > 128 || T > (1 << 24) || B > (1 << 24)) return PISA_ERR_UNSUPPORTED;
+  if (!(scale >= 0.f) || !std::isfinite(scale) || (flags & ~(PISA_CAUSAL | PISA_ZERO_TAIL))) return PISA_ERR_INVALID_ARG;
+  if (!cu_seqlens || ((uintptr_t)cu_seqlens & 3u)) return PISA_ERR_INVALID_ARG;
+  if (T == 0) return PISA_OK;
+  PISA_TRY(check_rows(q, Hq, T, d, false));
+  PISA_TRY(check_rows(k, Hkv, T, d, false));
+  PISA_TRY(check_rows(v, Hkv, T, d, false));
+  PISA_TRY(check_rows(dout, Hq, T, d, false));
+  PISA_TRY(check_rows(dq, Hq, T, d, true));
+  PISA_TRY(check_rows(dk, Hkv, T, d, true));
+  PISA_TRY(check_rows(dv, Hkv, T, d, true));
+  if (!lse || ((uintptr_t)lse & 3u) || !aligned16(out_f32) || !aligned16(workspace)) return PISA_ERR_INVALID_ARG;
+  const void *in[] = {q.data, k.data, v.data, dout.data, out_f32, lse};
+  const void *out[] = {dq.data, dk.data, dv.data};
+  for (const void *o : out)
+    for (const void *i : in)
+      if (o == i) return PISA_ERR_INVALID_ARG;
+  if (out[0] == out[1] || out[0] == out[2] || out[1] == out[2]) return PISA_ERR_INVALID_ARG;
+  if (ws_bytes < packed_bwd_layout(T, Hq, d).total) return PISA_ERR_WORKSPACE;
+  PackedProblem p{};
+  p.cu = cu_seqlens;
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.causal = flags & PISA_CAUSAL;
+  p.max_kv = T;
+  const float s = scale == 0.f ? 1.f / std::sqrt((float)d) : scale;
+  unsigned char *ws = (unsigned char *)workspace;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int clear = flags & PISA_ZERO_TAIL;
+  if (d == 128) return launch_packed_bwd<128>(p, q, k, v, dout, lse, out_f32, s, dq, dk, dv, clear, ws, st);
+  return launch_packed_bwd<64>(p, q, k, v, dout, lse, out_f32, s, dq, dk, dv, clear, ws, st);
+}
+
+}  // extern "C"

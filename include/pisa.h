@@ -72,7 +72,8 @@ typedef enum {
                         attention: every K/V block is read. */
 } pisa_mode;
 
-typedef enum { PISA_BF16 = 0, PISA_F32 = 1 } pisa_dtype;
+/* PISA_F16: packed sequences and the paged cache only (forward). */
+typedef enum { PISA_BF16 = 0, PISA_F32 = 1, PISA_F16 = 2 } pisa_dtype;
 
 /* sink_idx values: the authors' README, "Attention sink for MMDiT": 0 or -1
  * force the first or the last K/V block into the exact set of every query
@@ -276,6 +277,137 @@ pisa_status pisa_dense_attention(const void *q, const void *k, const void *v, vo
                                  pisa_dtype dtype, int B, int H, int L, int d, float scale,
                                  void *workspace, size_t ws_bytes, pisa_stream_t stream);
 size_t pisa_dense_attention_workspace_bytes(int B, int H, int L, int d, pisa_dtype dtype);
+
+/* ---- packed sequences and a paged key/value cache -------------------------- */
+
+/* Softmax attention for language models beside the dense baseline above:
+ * sequences of different lengths packed into one tensor, causal masks, grouped
+ * key heads, and keys and values that live in pages.
+ *
+ * Common to the calls of this section:
+ *  - A packed tensor is [H][T] rows of d elements (d contiguous), each row at
+ *    data + head * head_stride + row * row_stride (pisa_rows), so [H, T, d],
+ *    [T, H, d] and slices of a fused projection are all taken in place.
+ *    Strides count elements, are multiples of 8 and at least d; data is 16-byte
+ *    aligned; the stride of an extent of one is not used.
+ *  - Sequence b holds rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device
+ *    int32 [B + 1], ascending, within [0, T]); a sequence may be empty.  Rows
+ *    behind the last sequence are neither read into any result nor written
+ *    (unless PISA_ZERO_TAIL is set).
+ *  - Query head h reads key head h / (Hq / Hkv); Hq is a multiple of Hkv, and
+ *    Hq / Hkv at most 128.  d is 64 or 128.  dtype is PISA_BF16 or PISA_F16
+ *    (gradients: PISA_BF16); scores, maxima, sums and accumulators are float32,
+ *    softmax weights are rounded to dtype for their product with the values.
+ *  - Lengths, offsets and tables stay on the device: a captured call serves
+ *    whatever they hold at replay.  What is out of range is clamped or left
+ *    out, never followed out of bounds, and recorded in the status word
+ *    (PISA_ERR_DEVICE from pisa_device_status); results of such a call are
+ *    unspecified.
+ *  - A row that sees no key is zero, its lse is -infinity.  Memory behind a
+ *    sequence's last key may hold anything, NaN included.  A non-finite key or
+ *    value inside a sequence may reach any row of that sequence (and head
+ *    group), masked or not, but no other sequence.
+ *  - Results do not depend on timing: no atomics, a fixed order of every sum.
+ *    `workspace` is scratch of one call; calls that may overlap need one each. */
+typedef struct {
+  void *data;
+  int64_t head_stride, row_stride; /* elements */
+} pisa_rows;
+
+/* [num_pages][Hkv][page_size] rows of d elements: position j of a request is
+ * row j % page_size of page block_table[j / page_size].  page_size is 16, 32,
+ * 64, 128 or 256.  Alignment and strides as for pisa_rows. */
+typedef struct {
+  void *data;
+  int64_t page_stride, head_stride, row_stride; /* elements */
+} pisa_pages;
+
+/* flags of the varlen calls */
+#define PISA_CAUSAL 1    /* token i sees tokens 0 .. i; else all of its sequence */
+#define PISA_ZERO_TAIL 2 /* rows behind the last sequence are set to zero (out, dq, dk, dv;
+                            not lse and out_f32) instead of left as they were */
+
+size_t pisa_varlen_attention_workspace_bytes(int Hq, int Hkv, int d);
+
+/* Every sequence of a packed batch over itself: token i of a sequence sees its
+ * tokens 0 .. i (causal) or all of them.
+ *   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(s q_t . k_j)
+ * q, out: [Hq][T]; k, v: [Hkv][T].  lse (may be NULL): float32 [Hq, T], ln of
+ * the sum.  out_f32 (may be NULL; 16-byte aligned): float32 [Hq, T, d], the
+ * output before its rounding, which the backward needs.  out overlaps no input. */
+pisa_status pisa_varlen_attention(pisa_rows q, pisa_rows k, pisa_rows v, pisa_dtype dtype,
+                                  const int32_t *cu_seqlens, int B, int T, int Hq, int Hkv, int d,
+                                  float scale, int flags, pisa_rows out, float *lse, float *out_f32,
+                                  void *workspace, size_t ws_bytes, pisa_stream_t stream);
+
+size_t pisa_varlen_attention_bwd_workspace_bytes(int T, int Hq, int Hkv, int d);
+
+/* Gradients of pisa_varlen_attention: given dout = dL/d out writes dq, dk, dv
+ * (a key head's from every query head of its group).  bf16 only: dS = P (dP -
+ * Delta) has no scale of its own and would underflow in f16.  lse and out_f32
+ * from one forward call on the same inputs that was given both (its denominator
+ * then sums the rounded weights, see pisa_sparse_attention_fwd).  dq, dk, dv
+ * overlap no input and one another not. */
+pisa_status pisa_varlen_attention_bwd(pisa_rows q, pisa_rows k, pisa_rows v, pisa_rows dout,
+                                      pisa_dtype dtype, const float *lse, const float *out_f32,
+                                      const int32_t *cu_seqlens, int B, int T, int Hq, int Hkv,
+                                      int d, float scale, int flags, pisa_rows dq, pisa_rows dk,
+                                      pisa_rows dv, void *workspace, size_t ws_bytes,
+                                      pisa_stream_t stream);
+
+size_t pisa_paged_attention_workspace_bytes(int Hq, int Hkv, int d);
+
+/* The newest tokens of every request over its pages (which hold their keys and
+ * values already): the n = cu_seqlens[b + 1] - cu_seqlens[b] tokens of request b
+ * are the last n of its kv_lens[b] positions, token i sees positions
+ * 0 .. kv_lens[b] - n + i.  block_table: device int32 [B, width]; only entries of
+ * pages that hold a position are read.  lse as above. */
+pisa_status pisa_paged_attention(pisa_rows q, pisa_pages k_cache, pisa_pages v_cache,
+                                 pisa_dtype dtype, int num_pages, int page_size,
+                                 const int32_t *block_table, int width, const int32_t *cu_seqlens,
+                                 const int32_t *kv_lens, int B, int T, int Hq, int Hkv, int d,
+                                 float scale, pisa_rows out, float *lse, void *workspace,
+                                 size_t ws_bytes, pisa_stream_t stream);
+
+/* One step's bookkeeping, all device memory except the struct itself. */
+typedef struct {
+  const int32_t *past_lens; /* [B] positions that each request holds */
+  const int32_t *new_lens;  /* [B] tokens that it gets */
+  int B, T;                 /* requests (at most 16384); rows of `slots` */
+  int32_t *block_table;     /* [B, width], entries of new pages are written */
+  int width, page_size;
+  const int32_t *free_pages; /* [free_cap], pages are taken from entry num_free - 1 downwards */
+  int free_cap;
+  const int32_t *num_free; /* [1] */
+  int64_t *slots;          /* out [T]: page * page_size + row of each new token, -1 behind them */
+  int32_t *cu_seqlens;     /* out [B + 1] */
+  int32_t *kv_lens;        /* out [B]: past + new */
+  int32_t *num_free_out;   /* out [1] */
+} pisa_page_step;
+
+/* Block tables and slots of one step from the requests' lengths.  Request b
+ * needs ceil((past + new) / page_size) - ceil(past / page_size) new pages;
+ * requests take theirs in order.  All or nothing: if a length is negative, a
+ * request outgrows the table's width, the new tokens outgrow T or the pages run
+ * out, the table and the counts stay as they are, every slot is -1, cu_seqlens
+ * is all 0, kv_lens = past_lens, and the status word records it.  Outputs
+ * overlap no input and no other output (the table aside, which is both). */
+pisa_status pisa_page_plan(const pisa_page_step *step, pisa_stream_t stream);
+
+/* Rows t of k and v (packed, [Hkv][T]) to their slots of the caches; rows with a
+ * negative slot are left out, a slot past the caches is left out and recorded.
+ * Slots are distinct (rows of equal slots leave an unspecified mix).  The caches
+ * overlap neither k, v nor one another. */
+pisa_status pisa_page_write(pisa_rows k, pisa_rows v, pisa_dtype dtype, const int64_t *slots, int T,
+                            int Hkv, int d, pisa_pages k_cache, pisa_pages v_cache, int num_pages,
+                            int page_size, pisa_stream_t stream);
+
+/* The whole step: pisa_page_plan, pisa_page_write of k and v, and
+ * pisa_paged_attention of q, in order on `stream`. */
+pisa_status pisa_paged_step(const pisa_page_step *step, pisa_rows q, pisa_rows k, pisa_rows v,
+                            pisa_pages k_cache, pisa_pages v_cache, pisa_dtype dtype, int num_pages,
+                            int Hq, int Hkv, int d, float scale, pisa_rows out, float *lse,
+                            void *workspace, size_t ws_bytes, pisa_stream_t stream);
 
 /* ---- block statistics without any allocation ----------------------------- */
 
