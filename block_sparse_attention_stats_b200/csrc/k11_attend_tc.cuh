@@ -11,12 +11,15 @@
 // Work unit (packed_schedule.cuh): two subtiles of 128 rows, each 128 / G tokens
 // with the G query heads of one key head (token-major), so K and V are read once
 // for a group.  Keys come in tiles of 128.
-// Roles (320 threads, one CTA per SM, persistent over its range of tiles):
+// Roles (384 threads, one CTA per SM, persistent over its range of tiles):
 //   warp 0      copies: Q of both subtiles, then K and V tiles into a ring;
 //   warp 1      TMEM; issues S_i = Q_i K^T and O_i += P_i V (P read from TMEM);
 //               subtile 0's products run while subtile 1's softmax does, and back;
-//   warps 2-5   softmax of subtile 0, one thread a row (TMEM lane);
-//   warps 6-9   softmax of subtile 1.
+//   warps 4-7   softmax of subtile 0, one thread a row (TMEM lane);
+//   warps 8-11  softmax of subtile 1.
+// A softmax thread holds 128 scores: its warpgroups take 200 registers a thread,
+// the first (whose warps 2 and 3 have nothing to do) keeps 104: with the launch's
+// 168 for all, the scores spilled.
 // TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 after it;
 // P (16-bit) overwrites the first 64 columns of its S.  S_i of the next tile is
 // issued after P_i V of this one by the same thread, and one thread's products
@@ -36,7 +39,9 @@
 namespace pisa {
 
 template <int D> struct AttendCfg {
-  static constexpr int kThreads = 320;
+  static constexpr int kThreads = 384;
+  static constexpr int kRegsSoftmax = 200, kRegsOther = 104;   // of 168 at launch
+  static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "registers");
   static constexpr int kRows = 256;                      // rows of a unit
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kTileBytes = kKeyTile * D * 2;    // K or V tile, or Q of a subtile
@@ -68,7 +73,7 @@ __device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedS
 }
 
 template <typename T, int D, bool PAGED>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(384, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PackedProblem p,
                      const PagedKV cache, float scale, const PackedOut o,
@@ -134,6 +139,8 @@ __global__ void __launch_bounds__(320, 1)
   };
   auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort != 0); };
 
+  if (warp < 4) {
+  regs_shrink<C::kRegsOther>();
   if (warp == 0) {
     // ======================= copies ============================================
     const int page_rows = PAGED ? min(cache.page_size, kKeyTile) : kKeyTile;
@@ -323,9 +330,11 @@ __global__ void __launch_bounds__(320, 1)
       commit(C::kBarTeardown);
       uwait(bar(C::kBarTeardown), 0);
     }
+  }
   } else {
     // ======================= softmax ===========================================
-    const int i = (warp - 2) >> 2;             // subtile
+    regs_grow<C::kRegsSoftmax>();
+    const int i = (warp - 4) >> 2;             // subtile
     const int sp = warp & 3;                   // TMEM sub-partition of this warp
     const int row = sp * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(sp * 32) << 16);
@@ -486,7 +495,7 @@ __global__ void __launch_bounds__(320, 1)
         tc_fence_before();
         mbar_arrive(bar(C::kBarOFree + i));
       }
-      if (!whole && s.ta == 0 && tid == 64) cuts[blockIdx.x] = packed_cut(*start, s);
+      if (!whole && s.ta == 0 && tid == 128) cuts[blockIdx.x] = packed_cut(*start, s);
     }
     if (!ok) *abort = 1;
   }

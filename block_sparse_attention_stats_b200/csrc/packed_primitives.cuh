@@ -20,6 +20,15 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Registers a thread, from here on; every warp of a warpgroup (four warps, the first a
+// multiple of four).  The shares of a CTA's warpgroups add up to what it was launched with.
+template <int N> __device__ __forceinline__ void regs_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // kind::f16 instruction descriptor with f16 or bf16 A and B, f32 accumulator
 template <bool kBf16> __host__ __device__ constexpr uint32_t idesc_16_f32(int M, int N, int a_mn, int b_mn) {
   return kBf16 ? idesc_bf16_f32(M, N, a_mn, b_mn)

@@ -9,6 +9,9 @@
 // so every CTA gets the same number of tiles whatever the lengths are.  Nothing
 // is read on the host: the cut depends on lengths in device memory alone, and
 // the grid on the device alone, so a captured launch serves any lengths.
+// A unit counts unit_cost tiles more than it has, for what its start and its end
+// take: without, a CTA that got many short units ran twice as long as the others.
+// A cut that would fall into these is moved to the unit's start.
 // A unit inside one range is written by its CTA.  A unit cut by a range's end
 // leaves float32 partial sums, and combine_kernel joins them in ascending CTA
 // order (no atomics: the same inputs give the same bits).
@@ -31,6 +34,7 @@ struct PackedProblem {
   int tq;                   // tokens of a row tile
   int max_kv;               // most key positions a sequence can have (table width x page size)
   int min_tiles;            // no range is cut shorter than this
+  int unit_cost;            // what a unit takes beside its tiles, in tiles
 };
 
 struct PackedRequest {
@@ -117,9 +121,15 @@ struct KeyCost {
   }
 };
 
+// what all key heads' units before row tile rt count
+template <class Cost>
+__host__ __device__ __forceinline__ long long packed_before(const PackedProblem &p, const PackedRequest &r, int rt) {
+  return p.Hkv * (Cost::before(p, r.n, r.kv, rt) + (long long)rt * p.unit_cost);
+}
+
 template <class Cost>
 __device__ __forceinline__ long long packed_cost(const PackedProblem &p, const PackedRequest &r) {
-  return (long long)p.Hkv * Cost::before(p, r.n, r.kv, Cost::units(p, r.n));
+  return packed_before<Cost>(p, r, Cost::units(p, r.n));
 }
 
 struct PackedStart {
@@ -204,23 +214,24 @@ struct PackedSegment {
 // hold the same values), so no role waits for another to learn what comes next.
 template <class Cost> struct PackedWalk {
   PackedSegment s;
-  long long left;
-  int t;         // first tile of the next segment inside its unit
+  long long left;   // of the range, counted like the units
+  int at;           // where the next segment starts in its unit, counted like the unit
+  static constexpr int kDone = -1;
   // all 32 lanes of a converged warp
   __device__ __forceinline__ void begin(const PackedProblem &p, const PackedStart &st) {
     left = st.w1 - st.w0;
-    t = 0;
+    at = 0;
     s.b = st.b;
     s.rt = 0;
     s.h = 0;
     if (left <= 0) return;
     s.r = packed_request(p, s.b);
-    // last row tile whose first key tile is at or before rem: 32-way search
+    // last row tile that starts at or before rem: 32-way search
     int lo = 0, hi = Cost::units(p, s.r.n);   // answer in [lo, hi)
     const int lane = threadIdx.x & 31;
     while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-      const bool ok = at < hi && p.Hkv * Cost::before(p, s.r.n, s.r.kv, at) <= st.rem;
+      const int step = (hi - lo + 31) / 32, x = lo + lane * step;
+      const bool ok = x < hi && packed_before<Cost>(p, s.r, x) <= st.rem;
       const unsigned m = __ballot_sync(0xffffffffu, ok);   // lane 0 always holds
       const int last = 31 - __clz(m);
       lo += last * step;
@@ -228,14 +239,14 @@ template <class Cost> struct PackedWalk {
     }
     s.rt = lo;
     s.nt = Cost::tiles(p, s.r.n, s.r.kv, lo);
-    const long long in = st.rem - p.Hkv * Cost::before(p, s.r.n, s.r.kv, lo);
-    s.h = (int)(in / s.nt);
-    t = (int)(in % s.nt);
+    const long long in = st.rem - packed_before<Cost>(p, s.r, lo);
+    s.h = (int)(in / (s.nt + p.unit_cost));
+    at = (int)(in % (s.nt + p.unit_cost));
   }
   __device__ __forceinline__ bool next(const PackedProblem &p) {
     if (left <= 0) return false;
-    if (t == kDone) {
-      t = 0;
+    if (at == kDone) {
+      at = 0;
       if (++s.h == p.Hkv) {
         s.h = 0;
         if (++s.rt >= Cost::units(p, s.r.n)) {
@@ -248,13 +259,14 @@ template <class Cost> struct PackedWalk {
         s.nt = Cost::tiles(p, s.r.n, s.r.kv, s.rt);
       }
     }
-    s.ta = t;
-    s.tb = (int)(left < s.nt - t ? t + left : s.nt);
-    left -= s.tb - s.ta;
-    t = s.tb == s.nt ? kDone : s.tb;
-    return true;
+    const int all = s.nt + p.unit_cost;
+    const int end = (int)(left < all - at ? at + left : all);
+    left -= end - at;
+    s.ta = max(at - p.unit_cost, 0);
+    s.tb = max(end - p.unit_cost, 0);
+    at = end == all ? kDone : end;
+    return s.tb > s.ta;   // else the range ends before the unit's first tile: the next CTA has it all
   }
-  static constexpr int kDone = -1;
 };
 
 // What a CTA says about the unit that its range's end cuts (slot 1)

@@ -49,7 +49,8 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
   using C = AttendCfg<D>;
   const int tq1 = 128 / p.G;
   p.tq = 2 * tq1;
-  p.min_tiles = 2;
+  p.min_tiles = 4;
+  p.unit_cost = 2;
   CUtensorMap mq;
   PISA_TRY(map_query(&mq, q, Half16<T>::kBf16, D, p.G, p.T, p.Hkv, tq1));
   const PackedScratch s = packed_scratch(D, C::kRows);
@@ -70,6 +71,7 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
   using C = RowsCfg<D, R>;
   p.tq = R / p.G;
   p.min_tiles = 1;
+  p.unit_cost = 1;
   const PackedScratch s = packed_scratch(D, R);
   PackedCut *cuts = (PackedCut *)(ws + s.cuts);
   float *part = (float *)(ws + s.part);

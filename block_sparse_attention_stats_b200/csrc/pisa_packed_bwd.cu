@@ -47,7 +47,8 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
       lse2, delta);
   PISA_TRY(check_launch());
   p.tq = 128 / p.G;
-  p.min_tiles = 2;
+  p.min_tiles = 4;
+  p.unit_cost = 2;
   CUtensorMap mq, mdo, mk, mv;
   PISA_TRY(map_query(&mq, q, true, D, p.G, p.T, p.Hkv, p.tq));
   PISA_TRY(map_query(&mdo, dout, true, D, p.G, p.T, p.Hkv, p.tq));

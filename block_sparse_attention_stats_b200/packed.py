@@ -9,7 +9,6 @@ work runs on the tensors' device, on `stream` or that device's current stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -21,21 +20,37 @@ from .api import _check, _require
 _DT = {torch.bfloat16: L.PISA_BF16, torch.float16: L.PISA_F16}
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Makes `device` and `stream` current, so that memory allocated for the call belongs to the
-    stream that uses it; yields the stream's handle."""
-    if device.type != "cuda":
+def _stream_of(t, stream):
+    """(stream handle, context or None): the context makes the tensor's device and `stream`
+    current, so that memory allocated for the call belongs to the stream that uses it."""
+    if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    if stream is not None and stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-    here = torch.cuda.current_device() == device.index
-    if stream is None and here:
-        yield torch.cuda.current_stream(device).cuda_stream
-    else:
-        with torch.cuda.device(device):
-            with torch.cuda.stream(stream or torch.cuda.current_stream(device)):
-                yield (stream or torch.cuda.current_stream(device)).cuda_stream
+    if stream is None and torch.cuda.current_device() == t.get_device():
+        return _raw_stream(t.get_device()), None
+    dev = t.device
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+    with torch.cuda.device(dev):
+        stream = stream or torch.cuda.current_stream(dev)
+    # entering a stream's context makes its device current too
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _call_on(t, stream, body):
+    """body(stream handle) with the tensor's device and the stream current."""
+    handle, context = _stream_of(t, stream)
+    if context is None:
+        return body(handle)
+    with context:
+        return body(handle)
+
+
+def _raw_stream(index) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the handle without the stream object around it, where this torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _strides_ok(t) -> bool:
@@ -43,7 +58,8 @@ def _strides_ok(t) -> bool:
         n <= 1 or (s >= t.shape[-1] and s % 8 == 0) for n, s in zip(t.shape[:-1], t.stride()))
 
 
-def _tensor(t, dims, like, name):
+def _refuse(t, dims, like, name):
+    """Why t cannot be taken; returns where only the quick check failed it."""
     if t.dim() != dims or t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} must be a {like.dtype} tensor of {dims} dimensions on {like.device}")
     if t.numel() and not _strides_ok(t):
@@ -52,51 +68,71 @@ def _tensor(t, dims, like, name):
 
 
 def _rows(t, like, name) -> L.PisaRows:
-    _tensor(t, 3, like, name)
-    return L.PisaRows(t.data_ptr(), t.stride(0), t.stride(1))
+    ptr = t.data_ptr()
+    st = t.stride()
+    if len(st) == 3:
+        h, r, c = st
+        if (c == 1 and not (h | r) & 7 and not ptr & 15 and h >= 8 and r >= 8 and t.dtype is like.dtype
+                and t.get_device() == like.get_device()):
+            d = t.shape[2]
+            if h >= d and r >= d:
+                return L.PisaRows(ptr, h, r)
+    _refuse(t, 3, like, name)
+    return L.PisaRows(ptr, st[0], st[1])
 
 
 def _pages(t, like, name) -> L.PisaPages:
-    _tensor(t, 4, like, name)
-    return L.PisaPages(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    ptr = t.data_ptr()
+    st = t.stride()
+    if len(st) == 4:
+        p, h, r, c = st
+        if (c == 1 and not (p | h | r) & 7 and not ptr & 15 and t.dtype is like.dtype
+                and t.get_device() == like.get_device()):
+            d = t.shape[3]
+            if p >= d and h >= d and r >= d:
+                return L.PisaPages(ptr, p, h, r)
+    _refuse(t, 4, like, name)
+    return L.PisaPages(ptr, st[0], st[1], st[2])
 
 
-def _ints(t, shape, name, device, dtype=torch.int32):
-    if t.device != device:
-        raise ValueError(f"{name} must live on {device}")
-    _require(t, shape, dtype, name)
+def _dense(t, shape, dtype, name, like) -> Optional[int]:
+    """Pointer of a dense array of that shape on like's device (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != like.get_device() or not t.is_contiguous():
+        if t.device != like.device:
+            raise ValueError(f"{name} must live on {like.device}")
+        _require(t, shape, dtype, name)
     return t.data_ptr()
+
+
+def _ints(t, shape, name, like):
+    if t is None:
+        raise ValueError(f"{name} is needed")
+    return _dense(t, shape, torch.int32, name, like)
 
 
 def _heads(q, k, v):
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or q.shape[1:] != k.shape[1:]:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks != v.shape or qs[1:] != ks[1:]:
         raise ValueError("q must be [Hq, T, d] and k, v [Hkv, T, d]")
     if q.dtype not in _DT:
         raise ValueError("q, k, v must share dtype bf16 or float16")
-    if k.shape[0] == 0 or q.shape[0] == 0 or q.shape[0] % k.shape[0]:
+    hq, T, d = qs
+    hkv = ks[0]
+    if hkv == 0 or hq == 0 or hq % hkv:
         raise ValueError("the number of query heads must be a multiple of the number of key heads")
-    return (*q.shape, k.shape[0])
+    return hq, T, d, hkv
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, like):
+    """(tensor, pointer, bytes) of the call's scratch memory."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
-
-
-def _size(t) -> int:
-    return t.numel() * t.element_size()
-
-
-def _f32(t, shape, name, device) -> Optional[int]:
-    if t is None:
-        return None
-    if t.device != device:
-        raise ValueError(f"{name} must live on {device}")
-    _require(t, shape, torch.float32, name)
-    return t.data_ptr()
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ---- packed sequences -----------------------------------------------------------
@@ -113,19 +149,24 @@ def pisa_varlen_attention(q, k, v, cu_seqlens, causal: bool = True, scale: Optio
     lib = L.load()
     Hq, T, d, Hkv = _heads(q, k, v)
     B = cu_seqlens.numel() - 1
-    with _on(q.device, stream) as st:
-        out = torch.empty_like(q) if out is None else out
-        if out.shape != q.shape:
+    flags = (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0)
+
+    def body(st):
+        o = torch.empty_like(q) if out is None else out
+        if o.shape != q.shape:
             raise ValueError("out must have the shape of q")
-        ws = _scratch(workspace, lib.pisa_varlen_attention_workspace_bytes(Hq, Hkv, d), q.device)
-        flags = (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0)
-        _check("pisa_varlen_attention", lib.pisa_varlen_attention(
+        ws, ptr, size = _scratch(workspace, lib.pisa_varlen_attention_workspace_bytes(Hq, Hkv, d), q)
+        status = lib.pisa_varlen_attention(
             _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"), _DT[q.dtype],
-            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q.device), B, T, Hq, Hkv, d,
-            0.0 if scale is None else float(scale), flags, _rows(out, q, "out"),
-            _f32(lse, (Hq, T), "lse", q.device), _f32(out_f32, (Hq, T, d), "out_f32", q.device),
-            ws.data_ptr(), _size(ws), st))
-    return out
+            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), B, T, Hq, Hkv, d,
+            0.0 if scale is None else float(scale), flags, _rows(o, q, "out"),
+            _dense(lse, (Hq, T), torch.float32, "lse", q),
+            _dense(out_f32, (Hq, T, d), torch.float32, "out_f32", q), ptr, size, st)
+        if status:
+            _check("pisa_varlen_attention", status)
+        return o
+
+    return _call_on(q, stream, body)
 
 
 def pisa_varlen_attention_bwd(q, k, v, dout, lse, out_f32, cu_seqlens, causal: bool = True,
@@ -142,20 +183,26 @@ def pisa_varlen_attention_bwd(q, k, v, dout, lse, out_f32, cu_seqlens, causal: b
     if lse is None or out_f32 is None:
         raise ValueError("the backward takes the forward's lse and out_f32")
     B = cu_seqlens.numel() - 1
-    with _on(q.device, stream) as st:
-        dq, dk, dv = grads if grads is not None else (torch.empty_like(x) for x in (q, k, v))
+    flags = (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0)
+
+    def body(st):
+        dq, dk, dv = grads if grads is not None else (torch.empty_like(q), torch.empty_like(k),
+                                                      torch.empty_like(v))
         if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
             raise ValueError("grads must have the shapes of q, k, v")
-        ws = _scratch(workspace, lib.pisa_varlen_attention_bwd_workspace_bytes(T, Hq, Hkv, d), q.device)
-        flags = (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0)
-        _check("pisa_varlen_attention_bwd", lib.pisa_varlen_attention_bwd(
+        ws, ptr, size = _scratch(workspace, lib.pisa_varlen_attention_bwd_workspace_bytes(T, Hq, Hkv, d), q)
+        status = lib.pisa_varlen_attention_bwd(
             _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"), _rows(dout, q, "dout"),
-            _DT[q.dtype], _f32(lse, (Hq, T), "lse", q.device),
-            _f32(out_f32, (Hq, T, d), "out_f32", q.device),
-            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q.device), B, T, Hq, Hkv, d,
+            _DT[q.dtype], _dense(lse, (Hq, T), torch.float32, "lse", q),
+            _dense(out_f32, (Hq, T, d), torch.float32, "out_f32", q),
+            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), B, T, Hq, Hkv, d,
             0.0 if scale is None else float(scale), flags, _rows(dq, q, "dq"), _rows(dk, q, "dk"),
-            _rows(dv, q, "dv"), ws.data_ptr(), _size(ws), st))
-    return dq, dk, dv
+            _rows(dv, q, "dv"), ptr, size, st)
+        if status:
+            _check("pisa_varlen_attention_bwd", status)
+        return dq, dk, dv
+
+    return _call_on(q, stream, body)
 
 
 class _VarlenAttention(torch.autograd.Function):
@@ -221,19 +268,23 @@ def pisa_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens,
         raise ValueError("q must be [Hq, T, d] with the caches' d, block_table [B, width]")
     Hq, T, _ = q.shape
     B, width = block_table.shape
-    with _on(q.device, stream) as st:
-        out = torch.empty_like(q) if out is None else out
-        if out.shape != q.shape:
+
+    def body(st):
+        o = torch.empty_like(q) if out is None else out
+        if o.shape != q.shape:
             raise ValueError("out must have the shape of q")
-        ws = _scratch(workspace, lib.pisa_paged_attention_workspace_bytes(Hq, Hkv, d), q.device)
-        _check("pisa_paged_attention", lib.pisa_paged_attention(
+        ws, ptr, size = _scratch(workspace, lib.pisa_paged_attention_workspace_bytes(Hq, Hkv, d), q)
+        status = lib.pisa_paged_attention(
             _rows(q, q, "q"), _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"),
-            _DT[q.dtype], pages, ps, _ints(block_table, (B, width), "block_table", q.device), width,
-            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q.device),
-            _ints(kv_lens, (B,), "kv_lens", q.device), B, T, Hq, Hkv, d,
-            0.0 if scale is None else float(scale), _rows(out, q, "out"),
-            _f32(lse, (Hq, T), "lse", q.device), ws.data_ptr(), _size(ws), st))
-    return out
+            _DT[q.dtype], pages, ps, _ints(block_table, (B, width), "block_table", q), width,
+            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), _ints(kv_lens, (B,), "kv_lens", q),
+            B, T, Hq, Hkv, d, 0.0 if scale is None else float(scale), _rows(o, q, "out"),
+            _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size, st)
+        if status:
+            _check("pisa_paged_attention", status)
+        return o
+
+    return _call_on(q, stream, body)
 
 
 def _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out):
@@ -242,18 +293,19 @@ def _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size
     dev = block_table.device
     B, width = block_table.shape
     if out is None:
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = dict(slots=torch.empty(T, dtype=torch.int64, device=dev),
-                   cu_seqlens=torch.empty(B + 1, **i32), kv_lens=torch.empty(B, **i32),
-                   num_free=torch.empty(1, **i32))
+        # the small results share one allocation
+        small = torch.empty(2 * B + 2, dtype=torch.int32, device=dev)
+        out = dict(slots=torch.empty(T, dtype=torch.int64, device=dev), cu_seqlens=small[:B + 1],
+                   kv_lens=small[B + 1:-1], num_free=small[-1:])
+    like = block_table
+    slots = out["slots"]
     step = L.PisaPageStep(
-        _ints(past_lens, (B,), "past_lens", dev), _ints(new_lens, (B,), "new_lens", dev), B, T,
-        _ints(block_table, (B, width), "block_table", dev), width, page_size,
-        _ints(free_pages, free_pages.shape, "free_pages", dev), free_pages.numel(),
-        _ints(num_free, (1,), "num_free", dev),
-        _ints(out["slots"], (T,), "slots", dev, torch.int64),
-        _ints(out["cu_seqlens"], (B + 1,), "cu_seqlens", dev),
-        _ints(out["kv_lens"], (B,), "kv_lens", dev), _ints(out["num_free"], (1,), "num_free", dev))
+        _ints(past_lens, (B,), "past_lens", like), _ints(new_lens, (B,), "new_lens", like), B, T,
+        _ints(block_table, (B, width), "block_table", like), width, page_size,
+        _ints(free_pages, free_pages.shape, "free_pages", like), free_pages.numel(),
+        _ints(num_free, (1,), "num_free", like), _dense(slots, (T,), torch.int64, "slots", like),
+        _ints(out["cu_seqlens"], (B + 1,), "cu_seqlens", like),
+        _ints(out["kv_lens"], (B,), "kv_lens", like), _ints(out["num_free"], (1,), "num_free", like))
     return step, out
 
 
@@ -263,10 +315,15 @@ def pisa_page_plan(past_lens, new_lens, block_table, free_pages, num_free, page_
     dict(slots int64 [T], cu_seqlens [B + 1], kv_lens [B], num_free [1]).  Pages come from the end
     of free_pages[: num_free]; `out` may pass preallocated results.  All lengths int32."""
     lib = L.load()
-    with _on(block_table.device, stream) as st:
-        step, out = _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out)
-        _check("pisa_page_plan", lib.pisa_page_plan(ctypes.byref(step), st))
-    return out
+
+    def body(st):
+        step, res = _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out)
+        status = lib.pisa_page_plan(ctypes.byref(step), st)
+        if status:
+            _check("pisa_page_plan", status)
+        return res
+
+    return _call_on(block_table, stream, body)
 
 
 def pisa_page_write(k, v, slots, k_cache, v_cache, stream=None) -> None:
@@ -276,11 +333,15 @@ def pisa_page_write(k, v, slots, k_cache, v_cache, stream=None) -> None:
     if k.dim() != 3 or k.shape != v.shape or k.shape[0] != Hkv or k.shape[2] != d:
         raise ValueError("k and v must be [Hkv, T, d] with the caches' Hkv and d")
     T = k.shape[1]
-    with _on(k.device, stream) as st:
-        _check("pisa_page_write", lib.pisa_page_write(
-            _rows(k, k, "k"), _rows(v, k, "v"), _DT[k.dtype],
-            _ints(slots, (T,), "slots", k.device, torch.int64), T, Hkv, d,
-            _pages(k_cache, k, "k_cache"), _pages(v_cache, k, "v_cache"), pages, ps, st))
+
+    def body(st):
+        status = lib.pisa_page_write(
+            _rows(k, k, "k"), _rows(v, k, "v"), _DT[k.dtype], _dense(slots, (T,), torch.int64, "slots", k),
+            T, Hkv, d, _pages(k_cache, k, "k_cache"), _pages(v_cache, k, "v_cache"), pages, ps, st)
+        if status:
+            _check("pisa_page_write", status)
+
+    _call_on(k, stream, body)
 
 
 def pisa_paged_step(q, k, v, k_cache, v_cache, past_lens, new_lens, block_table, free_pages, num_free,
@@ -296,15 +357,20 @@ def pisa_paged_step(q, k, v, k_cache, v_cache, past_lens, new_lens, block_table,
         raise ValueError("q, k, v must have the caches' Hkv and d")
     if block_table.device != q.device:
         raise ValueError(f"block_table must live on {q.device}")
-    with _on(q.device, stream) as st:
-        out = torch.empty_like(q) if out is None else out
-        if out.shape != q.shape:
+
+    def body(st):
+        o = torch.empty_like(q) if out is None else out
+        if o.shape != q.shape:
             raise ValueError("out must have the shape of q")
-        step, plan = _page_step(past_lens, new_lens, block_table, free_pages, num_free, ps, T, plan)
-        ws = _scratch(workspace, lib.pisa_paged_attention_workspace_bytes(Hq, Hkv, d), q.device)
-        _check("pisa_paged_step", lib.pisa_paged_step(
+        step, res = _page_step(past_lens, new_lens, block_table, free_pages, num_free, ps, T, plan)
+        ws, ptr, size = _scratch(workspace, lib.pisa_paged_attention_workspace_bytes(Hq, Hkv, d), q)
+        status = lib.pisa_paged_step(
             ctypes.byref(step), _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"),
             _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"), _DT[q.dtype], pages, Hq, Hkv,
-            d, 0.0 if scale is None else float(scale), _rows(out, q, "out"),
-            _f32(lse, (Hq, T), "lse", q.device), ws.data_ptr(), _size(ws), st))
-    return out, plan
+            d, 0.0 if scale is None else float(scale), _rows(o, q, "out"),
+            _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size, st)
+        if status:
+            _check("pisa_paged_step", status)
+        return o, res
+
+    return _call_on(q, stream, body)
