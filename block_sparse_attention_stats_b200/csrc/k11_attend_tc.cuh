@@ -43,20 +43,21 @@ template <int D> struct AttendCfg {
   static constexpr int kRegsSoftmax = 200, kRegsOther = 104;   // of 168 at launch
   static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "registers");
   static constexpr int kRows = 256;                      // rows of a unit
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kTileBytes = kKeyTile * D * 2;    // K or V tile, or Q of a subtile
   static constexpr int kBoxBytes = kKeyTile * 128;       // one 64-column box of 128 rows
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileBytes;
-  static constexpr int kOffMisc = kOffKV + kStages * kTileBytes;
+  static constexpr int kOffStage = kOffKV + kStages * kTileBytes;   // 4 KB a softmax warp
+  static constexpr int kOffMisc = kOffStage + 8 * 4096;
   static constexpr int kSmem = kOffMisc + 1024 + 1024;   // + alignment slack
   static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarFull = 2, kBarEmpty = kBarFull + kStages;
   static constexpr int kBarS = kBarEmpty + kStages;      // + subtile
-  static constexpr int kBarP = kBarS + 2;
-  static constexpr int kBarO = kBarP + 2;                // O complete
+  static constexpr int kBarP = kBarS + 2;                // P's first 64 columns; + 2: the rest
+  static constexpr int kBarO = kBarP + 4;                // O complete
   static constexpr int kBarOFree = kBarO + 2;            // O read
   static constexpr int kBarTeardown = kBarOFree + 2;
-  static_assert(kBarTeardown < 32 && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kBarTeardown < 48 && kSmem <= 227 * 1024, "shared memory");
   static constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 };
 
@@ -72,7 +73,116 @@ __device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedS
   return x;
 }
 
-template <typename T, int D, bool PAGED>
+// One row's part of a 128 x 128 tile: scores from TMEM, running maximum and sum,
+// weights back as 16 bits over the scores' first 64 columns, O rescaled where
+// the maximum has moved.  `seen` columns are visible.
+// A quarter of the exponentials as a polynomial on the multiply-add units did not
+// pay: 918 against 893 us on 12000 + 700 + 4608 causal tokens, level on 2 x 4096
+// uncut ones (the products and their shared-memory reads bound the tile).
+// ROUNDED (where the float32 output is wanted too): for the backward the sum takes the rounded weights: dout_t . o_t
+// is then the mean of dP under the weights themselves, and does not lose dP -
+// Delta to their rounding where one key holds nearly all the weight.  Otherwise
+// the sum keeps the float32 weights.
+template <typename T, int D, bool ROUNDED>
+__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float sl2, int seen,
+                                             uint32_t bar_p, float &m_run, float &l_run) {
+  using namespace sm100;
+  uint32_t r[128];
+  tmem_ld_x32(s_addr, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+  tmem_ld_x32(s_addr + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+  tmem_wait_ld();
+  tmem_ld_x32(s_addr + 64, reinterpret_cast<uint32_t(&)[32]>(r[64]));
+  tmem_ld_x32(s_addr + 96, reinterpret_cast<uint32_t(&)[32]>(r[96]));
+  auto sv = [&](int c) -> float { return __uint_as_float(r[c]); };
+  const bool masked = __any_sync(0xffffffffu, seen < kKeyTile);
+  if (masked) {
+#pragma unroll
+    for (int c = 0; c < 64; ++c) r[c] = c < seen ? r[c] : 0xff800000u;
+  }
+  float mx[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) mx[c] = max3f(sv(c), sv(c + 8), sv(c + 16));
+#pragma unroll
+  for (int k = 24; k < 56; k += 16)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) mx[c] = max3f(mx[c], sv(c + k), sv(c + k + 8));
+#pragma unroll
+  for (int c = 0; c < 8; ++c) mx[c] = fmaxf(mx[c], sv(c + 56));
+  tmem_wait_ld();
+  if (masked) {
+#pragma unroll
+    for (int c = 64; c < 128; ++c) r[c] = c < seen ? r[c] : 0xff800000u;
+  }
+#pragma unroll
+  for (int k = 64; k < 128; k += 16)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) mx[c] = max3f(mx[c], sv(c + k), sv(c + k + 8));
+  const float tmax = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+  const float m_t = tmax * sl2;
+  const bool grow = m_t > m_run + 8.0f;
+  const bool need_o = grow && m_run != -INFINITY;
+  if (__any_sync(0xffffffffu, need_o)) {
+    const float f = grow ? ex2_approx(m_run - m_t) : 1.0f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t ov[16];
+      tmem_ld_x16(o_addr + 16 * c, ov);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+      tmem_st_x16(o_addr + 16 * c, ov);
+    }
+    l_run *= need_o ? f : 1.f;
+  }
+  if (grow) m_run = m_t;
+  const float neg = m_run == -INFINITY ? 0.f : -m_run;   // no key seen yet: every weight is zero
+  const float2 sl2x2 = make_float2(sl2, sl2), neg2 = make_float2(neg, neg);
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int c = 64 * h + 32 * q + 2 * k;
+        const float2 z = fma2(make_float2(sv(c), sv(c + 1)), sl2x2, neg2);
+        const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+        pk[k] = Half16<T>::pack(e.x, e.y);
+        acc[k & 1] = add2(acc[k & 1], ROUNDED ? Half16<T>::unpack(pk[k]) : e);
+      }
+      tmem_st_x16(s_addr + 32 * h + 16 * q, pk);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar_p + 16 * h);
+  }
+  const float2 a2 = add2(acc[0], acc[1]);
+  l_run += a2.x + a2.y;
+}
+
+// Rows of a warp's 32 x 128 bytes (lane r holds row r as eight 16-byte chunks,
+// chunk(k)) to global memory, four whole rows an instruction, by way of 4 KB of
+// shared memory: a store of 16 bytes a row would touch 32 lines.  `at`: this
+// lane's row as an offset into dst; COLS values of it are written.
+template <int COLS, typename E, typename F>
+__device__ __forceinline__ void store_rows(unsigned char *stage, int lane, int rows, long long at, E *dst,
+                                           F chunk) {
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = chunk(k);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = 4 * k + (lane >> 3), ch = lane & 7;
+    const long long a = __shfl_sync(0xffffffffu, at, r);
+    const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+    if (r < rows) *reinterpret_cast<uint4 *>(dst + a + ch * (COLS / 8)) = v;
+  }
+}
+
+template <typename T, int D, bool PAGED, bool ROUNDED>
 __global__ void __launch_bounds__(384, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PackedProblem p,
@@ -85,16 +195,16 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char *smem = smem_raw + (sbase - raw);
   auto bar = [&](int i) -> uint32_t { return sbase + C::kOffMisc + 8 * i; };
-  PackedStart *start = reinterpret_cast<PackedStart *>(smem + C::kOffMisc + 256);
-  volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 320);
-  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc + 336);
-  long long *wsum = reinterpret_cast<long long *>(smem + C::kOffMisc + 384);
+  PackedStart *start = reinterpret_cast<PackedStart *>(smem + C::kOffMisc + 384);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + C::kOffMisc + 448);
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + C::kOffMisc + 464);
+  long long *wsum = reinterpret_cast<long long *>(smem + C::kOffMisc + 512);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int tq1 = p.tq / 2, sub_rows = tq1 * p.G;
 
   if (warp == 1) {
-    tmem_alloc(sbase + C::kOffMisc + 336, C::kTmemCols);
+    tmem_alloc(sbase + C::kOffMisc + 464, C::kTmemCols);
     tmem_relinquish();
   }
   if (tid == 0) {
@@ -107,6 +217,7 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::kBarS + i), 1);
       mbar_init(bar(C::kBarP + i), 128);
+      mbar_init(bar(C::kBarP + 2 + i), 128);
       mbar_init(bar(C::kBarO + i), 1);
       mbar_init(bar(C::kBarOFree + i), 128);
     }
@@ -213,7 +324,6 @@ __global__ void __launch_bounds__(384, 1)
     int slot = 0, seg = 0;
     int np[2] = {0, 0};      // P tiles waited for
     int no[2] = {0, 0};      // segments that used O
-    bool ok = true;
     // S_i of the tile whose K is in ring slot `ks`
     auto issue_s = [&](int i, int ks) {
       const uint64_t qd = smem_desc_sw128(sbase + C::kOffQ + i * C::kTileBytes, 16, 1024);
@@ -231,75 +341,106 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     };
     auto full = [&](int sl) { return uwait(bar(C::kBarFull + sl % C::kStages), (sl / C::kStages) & 1); };
-    while (ok && w.next(p)) {
-      const PackedSegment &s = w.s;
-      const int nt0 = min(subtile(p, s, tq1, 0).nt, s.tb), nt1 = min(subtile(p, s, tq1, 1).nt, s.tb);
-      if (aborted() || !uwait(bar(C::kBarQFull), seg & 1) || !full(slot)) {
+    // a segment: first tile, end, key positions of the request, tiles of each subtile
+    struct Part {
+      int ta, tb, kv, nt[2];
+    };
+    auto take = [&](Part &x) -> bool {
+      if (!w.next(p)) return false;
+      x.ta = w.s.ta;
+      x.tb = w.s.tb;
+      x.kv = w.s.r.kv;
+      x.nt[0] = min(subtile(p, w.s, tq1, 0).nt, x.tb);
+      x.nt[1] = min(subtile(p, w.s, tq1, 1).nt, x.tb);
+      return true;
+    };
+    Part cur, nxt;
+    bool have = take(cur), ok = true;
+    if (have) {
+      ok = uwait(bar(C::kBarQFull), 0) && full(0);
+      tc_fence_after();
+      if (ok) {
+        if (cur.ta < cur.nt[0]) issue_s(0, 0);
+        if (cur.ta < cur.nt[1]) issue_s(1, 0);
+        commit(C::kBarEmpty + 0);
+        if (cur.ta + 1 == cur.tb) commit(C::kBarQEmpty);
+      }
+    }
+    while (ok && have) {
+      if (aborted()) {
         ok = false;
         break;
       }
-      ++seg;
-      tc_fence_after();
-      if (s.ta < nt0) issue_s(0, slot);
-      if (s.ta < nt1) issue_s(1, slot);
-      commit(C::kBarEmpty + slot % C::kStages);
-      if (s.ta + 1 >= s.tb) commit(C::kBarQEmpty);
-      for (int t = s.ta; ok && t < s.tb; ++t, slot += 2) {
-        const bool more = t + 1 < s.tb;
+      bool have_n = false;
+      for (int t = cur.ta; t < cur.tb; ++t, slot += 2) {
+        // after P V of this tile comes S of the next one, which may be the next unit's first
+        const bool last = t + 1 == cur.tb;
+        if (last) have_n = take(nxt);
+        const bool more = !last || have_n;
         bool have_v = false, have_k = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int nt = i ? nt1 : nt0;
-          if (t >= nt) continue;
-          if (aborted() || !uwait(bar(C::kBarP + i), np[i] & 1)) {
-            ok = false;
-            break;
-          }
-          ++np[i];
-          if (!have_v) {
-            have_v = true;
-            if (!full(slot + 1)) {
+        for (int i = 0; ok && i < 2; ++i) {
+          const int nt = cur.nt[i];
+          if (t < nt) {
+            if (!uwait(bar(C::kBarP + i), np[i] & 1)) {
               ok = false;
               break;
             }
-            const int live = s.r.kv - t * kKeyTile;
-            if (live < kKeyTile) {
-              // rows past the sequence's last key may hold anything: zero, so that 0 x Inf or
-              // NaN never reaches a sum
-              const int z0 = max(live, 0);
-              unsigned char *v = smem + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes;
-              for (int e = lane; e < (kKeyTile - z0) * (D / 8); e += 32) {
-                const int row = z0 + e / (D / 8), ch = e % (D / 8);
-                *reinterpret_cast<uint4 *>(v + (ch >> 3) * C::kBoxBytes + row * 128 +
-                                           (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            if (!have_v) {
+              have_v = true;
+              if (!full(slot + 1)) {
+                ok = false;
+                break;
               }
-              fence_proxy_async();
+              const int live = cur.kv - t * kKeyTile;
+              if (live < kKeyTile) {
+                // rows past the sequence's last key may hold anything: zero, so that 0 x Inf or
+                // NaN never reaches a sum
+                const int z0 = max(live, 0);
+                unsigned char *v = smem + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes;
+                for (int e = lane; e < (kKeyTile - z0) * (D / 8); e += 32) {
+                  const int row = z0 + e / (D / 8), ch = e % (D / 8);
+                  *reinterpret_cast<uint4 *>(v + (ch >> 3) * C::kBoxBytes + row * 128 +
+                                             (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                __syncwarp();
+              }
+            }
+            if (t == cur.ta) {
+              // the first product of a unit overwrites O: its rows have been read
+              if (no[i] > 0 && !uwait(bar(C::kBarOFree + i), (no[i] - 1) & 1)) {
+                ok = false;
+                break;
+              }
+              ++no[i];
+            }
+            const uint64_t vd = smem_desc_sw128(
+                sbase + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes, C::kBoxBytes, 1024);
+            // P's first 64 columns are multiplied while the rest are still being formed
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (h == 1 && !uwait(bar(C::kBarP + 2 + i), np[i] & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                  mma_ts(tmem + C::kColO + D * i, tmem + C::kColS + 128 * i + 8 * k,
+                         vd + (uint64_t)((k * 2048) >> 4), kIdO, (t > cur.ta || k > 0) ? 1u : 0u);
+                if (h == 1 && t + 1 >= nt) tc_commit(bar(C::kBarO + i));
+              }
               __syncwarp();
             }
+            if (!ok) break;
+            ++np[i];
           }
-          if (t == s.ta) {
-            // the first product of a unit overwrites O: its rows have been read
-            if (no[i] > 0 && !uwait(bar(C::kBarOFree + i), (no[i] - 1) & 1)) {
-              ok = false;
-              break;
-            }
-            ++no[i];
-          }
-          tc_fence_after();
-          const uint64_t vd = smem_desc_sw128(
-              sbase + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes, C::kBoxBytes, 1024);
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kKeyTile / 16; ++k)
-              mma_ts(tmem + C::kColO + D * i, tmem + C::kColS + 128 * i + 8 * k,
-                     vd + (uint64_t)((k * 2048) >> 4), kIdO, (t > s.ta || k > 0) ? 1u : 0u);
-            if (t + 1 >= nt) tc_commit(bar(C::kBarO + i));
-          }
-          __syncwarp();
-          if (t + 1 < nt) {
+          if (last ? (have_n && nxt.ta < nxt.nt[i]) : t + 1 < nt) {
             if (!have_k) {
               have_k = true;
-              if (!full(slot + 2)) {
+              if ((last && !uwait(bar(C::kBarQFull), (seg + 1) & 1)) || !full(slot + 2)) {
                 ok = false;
                 break;
               }
@@ -309,20 +450,16 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
         if (!ok) break;
-        if (!have_v && !full(slot + 1)) {   // a tile of no subtile (cannot happen): keep the ring going
-          ok = false;
-          break;
-        }
         commit(C::kBarEmpty + (slot + 1) % C::kStages);
         if (more) {
-          if (!have_k && !full(slot + 2)) {
-            ok = false;
-            break;
-          }
           commit(C::kBarEmpty + (slot + 2) % C::kStages);
-          if (t + 2 >= s.tb) commit(C::kBarQEmpty);
+          if (last ? nxt.ta + 1 == nxt.tb : t + 2 == cur.tb) commit(C::kBarQEmpty);
         }
       }
+      if (!ok) break;
+      ++seg;
+      have = have_n;
+      cur = nxt;
     }
     if (!ok) {
       *abort = 1;
@@ -340,6 +477,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(sp * 32) << 16);
     const uint32_t s_addr = lane_addr + C::kColS + 128 * i, o_addr = lane_addr + C::kColO + D * i;
     const float sl2 = scale * kLog2e;
+    unsigned char *stage = smem + C::kOffStage + (warp - 4) * 4096;
     int ns = 0, no = 0;
     bool ok = true;
     while (ok && w.next(p)) {
@@ -352,88 +490,12 @@ __global__ void __launch_bounds__(384, 1)
       const int t1 = min(x.nt, s.tb);
       float m_run = -INFINITY, l_run = 0.f;
       for (int t = s.ta; t < t1; ++t, ++ns) {
-        if (aborted() || !uwait(bar(C::kBarS + i), ns & 1)) {
+        if (!uwait(bar(C::kBarS + i), ns & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float sv[128];
-        {
-          uint32_t r[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_x32(s_addr + 32 * c, r[c]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 128; ++c) sv[c] = __uint_as_float(r[c >> 5][c & 31]);
-        }
-        const int seen = lim - t * kKeyTile;
-        if (__any_sync(0xffffffffu, seen < kKeyTile)) {
-#pragma unroll
-          for (int c = 0; c < 128; ++c) sv[c] = c < seen ? sv[c] : -INFINITY;
-        }
-        float mx[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mx[c] = max3f(sv[c], sv[c + 8], sv[c + 16]);
-#pragma unroll
-        for (int k = 24; k < 120; k += 16)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) mx[c] = max3f(mx[c], sv[c + k], sv[c + k + 8]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) mx[c] = fmaxf(mx[c], sv[c + 120]);
-        const float tmax = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-        const float m_t = tmax * sl2;
-        const bool grow = m_t > m_run + 8.0f;
-        const bool need_o = grow && m_run != -INFINITY;
-        const float f = grow ? ex2_approx(m_run - m_t) : 1.0f;
-        if (__any_sync(0xffffffffu, need_o)) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld_x32(o_addr + 32 * c, ov);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-            tmem_st_x32(o_addr + 32 * c, ov);
-          }
-        }
-        if (grow) {
-          m_run = m_t;
-          l_run *= f;
-        }
-        const float neg = m_run == -INFINITY ? 0.f : -m_run;   // no key seen yet: every weight is zero
-        const float2 sl2x2 = make_float2(sl2, sl2), neg2 = make_float2(neg, neg);
-        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                         make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          // P is rounded to 16 bits for its product; the sum keeps the float32 weights
-          uint32_t pk[32];
-          if (PAGED || o.f32 == nullptr) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float2 z = fma2(make_float2(sv[64 * h + 2 * k], sv[64 * h + 2 * k + 1]), sl2x2, neg2);
-              const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-              acc[k & 3] = add2(acc[k & 3], e);
-              pk[k] = Half16<T>::pack(e.x, e.y);
-            }
-          } else {
-            // for the backward the sum takes the rounded weights: dout_t . o_t is then the mean of
-            // dP under the weights themselves, and does not lose dP - Delta to their rounding
-            // where one key holds nearly all the weight
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float2 z = fma2(make_float2(sv[64 * h + 2 * k], sv[64 * h + 2 * k + 1]), sl2x2, neg2);
-              pk[k] = Half16<T>::pack(ex2_approx(z.x), ex2_approx(z.y));
-              acc[k & 3] = add2(acc[k & 3], Half16<T>::unpack(pk[k]));
-            }
-          }
-          tmem_st_x32(s_addr + 32 * h, pk);
-        }
-        const float2 a2 = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-        l_run += a2.x + a2.y;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(bar(C::kBarP + i));
+        softmax_tile<T, D, ROUNDED>(s_addr, o_addr, sl2, lim - t * kKeyTile, bar(C::kBarP + i), m_run, l_run);
       }
       if (!ok) break;
       // ---- epilogue of the segment ----------------------------------------------
@@ -461,33 +523,39 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
       if (used) {
-        T *dst = reinterpret_cast<T *>(o.out) + head * o.head + token * o.row;
+        // rows of the warp that are stored, and where each goes
+        const int nrow = min(max(x.rows - sp * 32, 0), 32);
+        const long long at = (long long)head * o.head + (long long)token * o.row;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tmem_ld_x32(o_addr + 32 * c, ov);
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t ov[64];
+          tmem_ld_x32(o_addr + 64 * c, reinterpret_cast<uint32_t(&)[32]>(ov[0]));
+          tmem_ld_x32(o_addr + 64 * c + 32, reinterpret_cast<uint32_t(&)[32]>(ov[32]));
           tmem_wait_ld();
-          if (!store) continue;
           if (whole) {
-            float v[32];
+            if (ROUNDED) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(ov[k]) * inv;
+              for (int k = 0; k < 64; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * inv);
+              store_rows<32>(stage, lane, nrow, (long long)hr * D + 64 * c, o.f32,
+                             [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
+              store_rows<32>(stage, lane, nrow, (long long)hr * D + 64 * c + 32, o.f32, [&](int k) {
+                return make_uint4(ov[32 + 4 * k], ov[33 + 4 * k], ov[34 + 4 * k], ov[35 + 4 * k]);
+              });
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              reinterpret_cast<uint4 *>(dst + 32 * c)[k] = make_uint4(
-                  Half16<T>::pack(v[8 * k], v[8 * k + 1]), Half16<T>::pack(v[8 * k + 2], v[8 * k + 3]),
-                  Half16<T>::pack(v[8 * k + 4], v[8 * k + 5]), Half16<T>::pack(v[8 * k + 6], v[8 * k + 7]));
-            if (o.f32) {
-              float4 *d32 = reinterpret_cast<float4 *>(o.f32 + hr * D + 32 * c);
+              for (int k = 0; k < 32; ++k)
+                ov[k] = Half16<T>::pack(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1]));
+            } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                d32[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+              for (int k = 0; k < 32; ++k)
+                ov[k] = Half16<T>::pack(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
             }
-          } else {
+            store_rows<64>(stage, lane, nrow, at + 64 * c, reinterpret_cast<T *>(o.out),
+                           [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
+          } else if (store) {
             float4 *ps = reinterpret_cast<float4 *>(slot + 2 * C::kRows);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              ps[(size_t)(8 * c + k) * C::kRows + prow] =
+            for (int k = 0; k < 16; ++k)
+              ps[(size_t)(16 * c + k) * C::kRows + prow] =
                   make_float4(__uint_as_float(ov[4 * k]), __uint_as_float(ov[4 * k + 1]),
                               __uint_as_float(ov[4 * k + 2]), __uint_as_float(ov[4 * k + 3]));
           }

@@ -138,10 +138,10 @@ __global__ void __launch_bounds__(320, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if (!KV)   // rows of the Q and dout tiles that no copy fills (128 is no multiple of G): zero
-    for (int e = tid; e < 2 * (128 - sub_rows) * (D / 8); e += C::kThreads) {
-      const int ch = e % (D / 8), row = sub_rows + (e / (D / 8)) % (128 - sub_rows),
-                i = e / ((D / 8) * (128 - sub_rows));
+  if constexpr (!KV)   // rows of the Q and dout tiles that no copy fills (128 is no multiple of G): zero
+    for (int e = tid; e < 256 * (D / 8); e += C::kThreads) {
+      const int ch = e % (D / 8), row = (e / (D / 8)) % 128, i = e / ((D / 8) * 128);
+      if (row < sub_rows) continue;
       *reinterpret_cast<uint4 *>(smem + C::kOffA + i * C::kTileBytes + (ch >> 3) * C::kBoxBytes + row * 128 +
                                  ((ch & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
     }

@@ -42,23 +42,25 @@ static pisa_status launch_combine(const PackedProblem &p, const PackedCut *cuts,
   return check_launch();
 }
 
-template <typename T, int D, bool PAGED>
+template <typename T, int D, bool PAGED, bool ROUNDED>
 static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_rows &q, const CUtensorMap &mk,
                              const CUtensorMap &mv, float scale, const PackedOut &o, int clear,
                              unsigned char *ws, cudaStream_t st) {
   using C = AttendCfg<D>;
   const int tq1 = 128 / p.G;
   p.tq = 2 * tq1;
-  p.min_tiles = 4;
-  p.unit_cost = 2;
+  // a unit's start and end take about two tiles, four with the float32 output (measured: 2 / 3 / 4 give
+  // 872 / 876 / 881 us on 12000 + 700 + 4608 tokens, and 2521 / 2430 us a training step at 2 / 3)
+  p.unit_cost = ROUNDED ? 4 : 2;
+  p.min_tiles = p.unit_cost + 1;
   CUtensorMap mq;
   PISA_TRY(map_query(&mq, q, Half16<T>::kBf16, D, p.G, p.T, p.Hkv, tq1));
   const PackedScratch s = packed_scratch(D, C::kRows);
   PackedCut *cuts = (PackedCut *)(ws + s.cuts);
   float *part = (float *)(ws + s.part);
-  PISA_CUDA(cudaFuncSetAttribute(attend_tc_kernel<T, D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  PISA_CUDA(cudaFuncSetAttribute(attend_tc_kernel<T, D, PAGED, ROUNDED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem));
-  attend_tc_kernel<T, D, PAGED><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(mq, mk, mv, p, cache, scale, o,
+  attend_tc_kernel<T, D, PAGED, ROUNDED><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(mq, mk, mv, p, cache, scale, o,
                                                                             cuts, part);
   PISA_TRY(check_launch());
   return launch_combine<T, D>(p, cuts, part, C::kRows, o, clear, st);
@@ -90,7 +92,8 @@ static pisa_status run_varlen(const PackedProblem &p, const pisa_rows &q, const 
   CUtensorMap mk, mv;
   PISA_TRY(map_rows(&mk, k, Half16<T>::kBf16, D, p.T, p.Hkv, kKeyTile));
   PISA_TRY(map_rows(&mv, v, Half16<T>::kBf16, D, p.T, p.Hkv, kKeyTile));
-  return launch_tc<T, D, false>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
+  if (o.f32) return launch_tc<T, D, false, true>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
+  return launch_tc<T, D, false, false>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
 }
 
 template <typename T, int D>
@@ -107,7 +110,7 @@ static pisa_status run_paged(const PackedProblem &p, const PagedKV &cache, const
   if (r <= 16) return launch_rows<T, D, 16>(p, cache, q, mk, mv, scale, o, ws, st);
   if (r <= 32) return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
   if (r <= 64) return launch_rows<T, D, 64>(p, cache, q, mk, mv, scale, o, ws, st);
-  return launch_tc<T, D, true>(p, cache, q, mk, mv, scale, o, 0, ws, st);
+  return launch_tc<T, D, true, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
 }
 
 // ---- argument checks --------------------------------------------------------------------
