@@ -161,27 +161,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
   l_run += a2.x + a2.y;
 }
 
-// Rows of a warp's 32 x 128 bytes (lane r holds row r as eight 16-byte chunks,
-// chunk(k)) to global memory, four whole rows an instruction, by way of 4 KB of
-// shared memory: a store of 16 bytes a row would touch 32 lines.  `at`: this
-// lane's row as an offset into dst; COLS values of it are written.
-template <int COLS, typename E, typename F>
-__device__ __forceinline__ void store_rows(unsigned char *stage, int lane, int rows, long long at, E *dst,
-                                           F chunk) {
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = chunk(k);
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int r = 4 * k + (lane >> 3), ch = lane & 7;
-    const long long a = __shfl_sync(0xffffffffu, at, r);
-    const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-    if (r < rows) *reinterpret_cast<uint4 *>(dst + a + ch * (COLS / 8)) = v;
-  }
-}
-
 template <typename T, int D, bool PAGED, bool ROUNDED>
 __global__ void __launch_bounds__(384, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -536,9 +515,9 @@ __global__ void __launch_bounds__(384, 1)
             if (ROUNDED) {
 #pragma unroll
               for (int k = 0; k < 64; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * inv);
-              store_rows<32>(stage, lane, nrow, (long long)hr * D + 64 * c, o.f32,
+              store_rows<8>(stage, lane, nrow, (long long)hr * D + 64 * c, o.f32,
                              [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
-              store_rows<32>(stage, lane, nrow, (long long)hr * D + 64 * c + 32, o.f32, [&](int k) {
+              store_rows<8>(stage, lane, nrow, (long long)hr * D + 64 * c + 32, o.f32, [&](int k) {
                 return make_uint4(ov[32 + 4 * k], ov[33 + 4 * k], ov[34 + 4 * k], ov[35 + 4 * k]);
               });
 #pragma unroll
@@ -549,7 +528,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int k = 0; k < 32; ++k)
                 ov[k] = Half16<T>::pack(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
             }
-            store_rows<64>(stage, lane, nrow, at + 64 * c, reinterpret_cast<T *>(o.out),
+            store_rows<8>(stage, lane, nrow, at + 64 * c, reinterpret_cast<T *>(o.out),
                            [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
           } else if (store) {
             float4 *ps = reinterpret_cast<float4 *>(slot + 2 * C::kRows);

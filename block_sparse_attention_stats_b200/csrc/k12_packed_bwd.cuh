@@ -9,10 +9,13 @@
 // every key tile: float32 atomics, whose order changes results, or a wait of
 // CTAs on one another.  Two kernels keep every sum in one CTA in a fixed order.
 //
-// Both keep a pair of 128-row tiles in shared memory (dq: Q and dout; dk, dv: K
-// and V) and stream the other pair through a ring, 128 rows at a time; both are
-// cut evenly over the SMs (packed_schedule.cuh), and sum_partials_kernel joins
-// what a range's end cuts.
+// Both keep a pair of 128-row tiles (dq: Q and dout; dk, dv: K and V) and stream
+// the other pair through a ring, 128 rows at a time; both are cut evenly over the
+// SMs (packed_schedule.cuh), and packed_sum_kernel joins what a range's end cuts.
+// dq keeps its pair in TMEM, as the A operands of S and dP: its products then read
+// half as much shared memory, and the ring has six tiles instead of four (with
+// four, K of the next tile arrived 600 cycles late).  dk, dv have two accumulators
+// and no TMEM left: their pair stays in shared memory.
 // Roles (320 threads): warp 0 copies; warp 1 issues every product; warps 2-5
 // take columns 0 .. 63 of each 128 x 128 tile, warps 6-9 columns 64 .. 127, one
 // thread a row (TMEM lane).
@@ -63,26 +66,25 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int D> struct PackedBwdCfg {
+template <int D, bool KV> struct PackedBwdCfg {
   static constexpr int kThreads = 320;
   static constexpr int kRows = 128;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? (KV ? 4 : 6) : (KV ? 8 : 12);
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kBoxBytes = 128 * 128;
-  static constexpr int kOffA = 0;                          // the resident pair
-  static constexpr int kOffRing = 2 * kTileBytes;
-  static constexpr int kOffMisc = kOffRing + kStages * kTileBytes;
-  static constexpr int kVecs = D == 128 ? 4 : 6;           // lse and Delta of streamed rows (dk, dv)
-  static constexpr int kOffVec = kOffMisc + 512;
-  static constexpr int kSmem = kOffMisc + 512 + 1024;      // dq; + alignment slack
-  static constexpr int kStagesKv = D == 128 ? 4 : 8;       // dk, dv: one stage less makes room for them
-  static constexpr int kOffMiscKv = kOffRing + kStagesKv * kTileBytes;
-  static constexpr int kSmemKv = kOffMiscKv + 512 + kVecs * 1024 + 1024;
-  static_assert(kSmem <= 227 * 1024 && kSmemKv <= 227 * 1024, "shared memory");
+  static constexpr int kOffA = 0;                          // the resident pair (KV)
+  static constexpr int kOffRing = KV ? 2 * kTileBytes : 0;
+  static constexpr int kOffStage = kOffRing + kStages * kTileBytes;   // 2 KB a warp that stores rows
+  static constexpr int kVecs = KV ? (D == 128 ? 4 : 6) : 1;           // lse and Delta of streamed rows (KV)
+  static constexpr int kOffVec = kOffStage + 8 * 2048;
+  static constexpr int kOffMisc = kOffVec + kVecs * 1024;
+  static constexpr int kSmem = kOffMisc + 1024 + 1024;     // + alignment slack
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  // kBarAFull: the resident pair is in shared memory (KV) or in TMEM; kBarAEmpty: KV only
   static constexpr int kBarAFull = 0, kBarAEmpty = 1, kBarS = 2, kBarDP = 3, kBarP = 4, kBarZ = 5, kBarAcc = 6,
-                       kBarAccFree = 7, kBarTeardown = 8, kBarFull = 9, kBarEmpty = kBarFull + 8;
-  static_assert(kBarEmpty + 8 <= 32, "barrier slots");
-  static constexpr uint32_t kTmemCols = 512, kColS = 0, kColDP = 128, kColAcc = 256;
+                       kBarAccFree = 7, kBarTeardown = 8, kBarFull = 9, kBarEmpty = kBarFull + kStages;
+  static_assert(kBarEmpty + kStages <= 48, "barrier slots");
+  static constexpr uint32_t kTmemCols = 512, kColS = 0, kColDP = 128, kColAcc = 256, kColA = 384;
 };
 
 // KV = false: dq.  The unit's rows are 128 / G tokens with the G heads of a key
@@ -98,32 +100,33 @@ __global__ void __launch_bounds__(320, 1)
                       long long out0_head, long long out0_row, __nv_bfloat16 *__restrict__ out1,
                       long long out1_head, long long out1_row, PackedCut *__restrict__ cuts,
                       float *__restrict__ part) {
-  using C = PackedBwdCfg<D>;
+  using C = PackedBwdCfg<D, KV>;
   using Cost = typename std::conditional<KV, KeyCost, RowCost<kKeyTile>>::type;
   using namespace sm100;
-  constexpr int kStages = KV ? C::kStagesKv : C::kStages;
-  constexpr int kMisc = KV ? C::kOffMiscKv : C::kOffMisc;
+  constexpr int kStages = C::kStages, kMisc = C::kOffMisc;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char *smem = smem_raw + (sbase - raw);
   auto bar = [&](int i) -> uint32_t { return sbase + kMisc + 8 * i; };
-  PackedStart *start = reinterpret_cast<PackedStart *>(smem + kMisc + 256);
-  volatile int *abort = reinterpret_cast<volatile int *>(smem + kMisc + 320);
-  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + kMisc + 336);
-  long long *wsum = reinterpret_cast<long long *>(smem + kMisc + 384);
-  float *vec = reinterpret_cast<float *>(smem + kMisc + 512);      // [kVecs][lse 128, Delta 128] (KV)
+  PackedStart *start = reinterpret_cast<PackedStart *>(smem + kMisc + 384);
+  volatile int *abort = reinterpret_cast<volatile int *>(smem + kMisc + 448);
+  volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + kMisc + 464);
+  long long *wsum = reinterpret_cast<long long *>(smem + kMisc + 512);
+  float *vec = reinterpret_cast<float *>(smem + C::kOffVec);      // [kVecs][lse 128, Delta 128] (KV)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int sub_rows = KV ? 128 : p.tq * p.G;
 
   if (warp == 1) {
-    tmem_alloc(sbase + kMisc + 336, C::kTmemCols);
+    tmem_alloc(sbase + kMisc + 464, C::kTmemCols);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i <= C::kBarTeardown; ++i)
-      mbar_init(bar(i), i == C::kBarP || i == C::kBarZ || i == C::kBarAccFree ? 256 : 1);
+      mbar_init(bar(i), i == C::kBarP || i == C::kBarZ || i == C::kBarAccFree || (!KV && i == C::kBarAFull)
+                            ? 256
+                            : 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(C::kBarFull + s), 1);
       mbar_init(bar(C::kBarEmpty + s), 1);
@@ -138,14 +141,6 @@ __global__ void __launch_bounds__(320, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if constexpr (!KV)   // rows of the Q and dout tiles that no copy fills (128 is no multiple of G): zero
-    for (int e = tid; e < 256 * (D / 8); e += C::kThreads) {
-      const int ch = e % (D / 8), row = (e / (D / 8)) % 128, i = e / ((D / 8) * 128);
-      if (row < sub_rows) continue;
-      *reinterpret_cast<uint4 *>(smem + C::kOffA + i * C::kTileBytes + (ch >> 3) * C::kBoxBytes + row * 128 +
-                                 ((ch & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-    }
-  fence_proxy_async();
   tc_fence_before();
   packed_locate<Cost>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
   tc_fence_after();
@@ -170,51 +165,79 @@ __global__ void __launch_bounds__(320, 1)
     // ======================= copies ============================================
     int slot = 0, seg = 0, tile = 0;
     bool ok = true;
+    auto room = [&]() -> bool {
+      return !aborted() && (slot < kStages || uwait(bar(C::kBarEmpty + slot % kStages), ((slot / kStages) - 1) & 1));
+    };
     while (ok && w.next(p)) {
       const PackedSegment &s = w.s;
-      if (aborted() || (seg > 0 && !uwait(bar(C::kBarAEmpty), (seg - 1) & 1))) {
-        ok = false;
-        break;
-      }
-      if (elect_one()) {
-        const uint32_t a = bar(C::kBarAFull);
-        mbar_expect_tx(a, 2 * sub_rows * D * 2);
+      if constexpr (KV) {
+        if (aborted() || (seg > 0 && !uwait(bar(C::kBarAEmpty), (seg - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          const uint32_t a = bar(C::kBarAFull);
+          mbar_expect_tx(a, 2 * C::kTileBytes);
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int b = 0; b < D / 64; ++b) {
-            const uint32_t dst = sbase + C::kOffA + x * C::kTileBytes + b * C::kBoxBytes;
-            if (KV)
-              tma_load_3d(dst, x ? &tm_v : &tm_k, a, 64 * b, s.r.first + s.rt * 128, s.h);
-            else
-              tma_load_4d(dst, x ? &tm_do : &tm_q, a, 64 * b, 0, s.r.first + s.rt * p.tq, s.h);
+            for (int b = 0; b < D / 64; ++b)
+              tma_load_3d(sbase + C::kOffA + x * C::kTileBytes + b * C::kBoxBytes, x ? &tm_v : &tm_k, a, 64 * b,
+                          s.r.first + s.rt * 128, s.h);
+        }
+        __syncwarp();
+        ++seg;
+      } else {
+        // Q and dout pass through two ring slots on their way to TMEM
+#pragma unroll
+        for (int x = 0; ok && x < 2; ++x) {
+          if (!room()) {
+            ok = false;
+            break;
           }
+          if (elect_one()) {
+            const uint32_t full = bar(C::kBarFull + slot % kStages);
+            mbar_expect_tx(full, sub_rows * D * 2);
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b)
+              tma_load_4d(sbase + C::kOffRing + (slot % kStages) * C::kTileBytes + b * C::kBoxBytes,
+                          x ? &tm_do : &tm_q, full, 64 * b, 0, s.r.first + s.rt * p.tq, s.h);
+          }
+          __syncwarp();
+          ++slot;
+        }
       }
-      __syncwarp();
-      ++seg;
       for (int t = s.ta; ok && t < s.tb; ++t, ++tile) {
         int g = 0;
         const int row0 = tile_at(s, t, g);
         const int head = KV ? s.h * p.G + g : s.h;
+        float lv[4], dv[4];
+        if constexpr (KV) {
+          // lse and Delta of the tile's rows: asked for before the wait for room
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = lane + 32 * k;
+            const bool in = row0 + r < s.r.n;
+            const size_t at = (size_t)head * p.T + s.r.first + row0 + r;
+            lv[k] = in ? lse2[at] : INFINITY;     // exp2(x - inf) = 0: a row that is not there
+            dv[k] = in ? delta[at] : 0.f;
+          }
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x, ++slot) {
-          const int st = slot % kStages;
-          if (aborted() || (slot >= kStages && !uwait(bar(C::kBarEmpty + st), ((slot / kStages) - 1) & 1))) {
+          if (!room()) {
             ok = false;
             break;
           }
+          const int st = slot % kStages;
           if (KV && x == 0) {
-            // lse and Delta of the tile's rows, before the arrival that hands the slot over.
-            // Buffer tile % kVecs was last read for tile - kVecs, whose dS came before the
-            // products that freed this slot
+            // handed over with the slot's arrival.  Buffer tile % kVecs was last read for tile -
+            // kVecs, whose dS came before the products that freed this slot
             float *v = vec + (tile % C::kVecs) * 256;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int r = lane + 32 * k;
-              const bool in = row0 + r < s.r.n;
-              const size_t at = (size_t)head * p.T + s.r.first + row0 + r;
-              v[r] = in ? lse2[at] : INFINITY;     // exp2(x - inf) = 0: a row that is not there
-              v[128 + r] = in ? delta[at] : 0.f;
+              v[lane + 32 * k] = lv[k];
+              v[128 + lane + 32 * k] = dv[k];
             }
             __syncwarp();
           }
@@ -233,7 +256,7 @@ __global__ void __launch_bounds__(320, 1)
     if (!ok) {
       *abort = 1;
       // copies in flight land before the CTA exits
-      if (seg > 0) uwait(bar(C::kBarAFull), (seg - 1) & 1);
+      if (KV && seg > 0) uwait(bar(C::kBarAFull), (seg - 1) & 1);
       for (int i = max(slot - kStages, 0); i < slot; ++i)
         uwait(bar(C::kBarFull + i % kStages), (i / kStages) & 1);
     }
@@ -272,8 +295,13 @@ __global__ void __launch_bounds__(320, 1)
       const uint64_t bd = smem_desc_sw128(ring(sl + x), 16, 1024);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + (x ? C::kColDP : C::kColS), ad + step(k), bd + step(k), kIdS, k > 0 ? 1u : 0u);
+        for (int k = 0; k < D / 16; ++k) {
+          if (KV)
+            mma_ss(tmem + (x ? C::kColDP : C::kColS), ad + step(k), bd + step(k), kIdS, k > 0 ? 1u : 0u);
+          else
+            mma_ts(tmem + (x ? C::kColDP : C::kColS), tmem + C::kColA + 64 * x + 8 * k, bd + step(k), kIdS,
+                   k > 0 ? 1u : 0u);
+        }
         tc_commit(bar(x ? C::kBarDP : C::kBarS));
       }
       __syncwarp();
@@ -295,7 +323,20 @@ __global__ void __launch_bounds__(320, 1)
       const PackedSegment &s = w.s;
       int g = 0;
       auto live = [&](int t) { return max(min(s.r.n - tile_at(s, t, g), 128), 0); };
-      if (aborted() || !uwait(bar(C::kBarAFull), seg & 1) || !take(slot, live(s.ta))) {
+      if (aborted() || !uwait(bar(C::kBarAFull), seg & 1)) {
+        ok = false;
+        break;
+      }
+      if (!KV) {
+        // Q and dout are in TMEM: their ring slots are free
+        if (elect_one()) {
+          mbar_arrive(bar(C::kBarEmpty + slot % kStages));
+          mbar_arrive(bar(C::kBarEmpty + (slot + 1) % kStages));
+        }
+        __syncwarp();
+        slot += 2;
+      }
+      if (!take(slot, live(s.ta))) {
         ok = false;
         break;
       }
@@ -306,7 +347,7 @@ __global__ void __launch_bounds__(320, 1)
       }
       issue_s(1, slot);
       if (!KV) commit(C::kBarEmpty + (slot + 1) % kStages);
-      if (s.ta + 1 == s.tb) commit(C::kBarAEmpty);
+      if (KV && s.ta + 1 == s.tb) commit(C::kBarAEmpty);
       for (int t = s.ta; t < s.tb; ++t, slot += 2, ++u) {
         const bool more = t + 1 < s.tb, first = t == s.ta;
         // P_u of dk, dv is in TMEM; S_u of dq is in registers
@@ -345,7 +386,7 @@ __global__ void __launch_bounds__(320, 1)
           }
           issue_s(1, slot + 2);
           if (!KV) commit(C::kBarEmpty + (slot + 3) % kStages);
-          if (t + 2 == s.tb) commit(C::kBarAEmpty);
+          if (KV && t + 2 == s.tb) commit(C::kBarAEmpty);
         } else {
           commit(C::kBarAcc);
         }
@@ -365,9 +406,38 @@ __global__ void __launch_bounds__(320, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(sp * 32) << 16);
     const uint32_t s_addr = lane_addr + C::kColS + 64 * gw, dp_addr = lane_addr + C::kColDP + 64 * gw;
     const float sl2 = scale * kLog2e;
-    int u = 0, seg = 0;
-    bool ok = true;
-    while (ok && w.next(p)) {
+    unsigned char *stage = smem + C::kOffStage + (warp - 2) * 2048;
+    int u = 0, seg = 0, slot = 0;
+    // this thread's row of Q (warpgroup 0) or dout (warpgroup 1) from the ring slots of segment
+    // w.s into TMEM, as packed pairs.  The products that read the pair before have completed: this
+    // thread has waited for the last S and dP
+    auto load_pair = [&]() -> bool {
+      const int sl = slot + gw;
+      if (!uwait(bar(C::kBarFull + sl % kStages), (sl / kStages) & 1)) return false;
+      const unsigned char *box = smem + C::kOffRing + (sl % kStages) * C::kTileBytes + row * 128;
+#pragma unroll
+      for (int b = 0; b < D / 64; ++b) {
+        uint32_t x[32];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row < sub_rows) v = *reinterpret_cast<const uint4 *>(box + b * C::kBoxBytes + ((c ^ (row & 7)) << 4));
+          x[4 * c] = v.x;
+          x[4 * c + 1] = v.y;
+          x[4 * c + 2] = v.z;
+          x[4 * c + 3] = v.w;
+        }
+        tmem_st_x32(lane_addr + C::kColA + 64 * gw + 32 * b, x);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(C::kBarAFull));
+      slot += 2 + 2 * (w.s.tb - w.s.ta);
+      return true;
+    };
+    bool have = w.next(p), ok = true;
+    if (!KV && have) ok = load_pair();
+    while (ok && have) {
       const PackedSegment s = w.s;
       int g = 0;
       // dq: this row's token, lse and Delta.  dk, dv: this row's key
@@ -461,6 +531,11 @@ __global__ void __launch_bounds__(320, 1)
         mbar_arrive(bar(C::kBarZ));
       }
       if (!ok) break;
+      have = w.next(p);
+      if (!KV && have && !load_pair()) {
+        ok = false;
+        break;
+      }
       // ---- epilogue: dq = s dQ (half of the columns a warpgroup); dk = s dK, dv = dV (one each) ----
       if (aborted() || !uwait(bar(C::kBarAcc), seg & 1)) {
         ok = false;
@@ -474,9 +549,11 @@ __global__ void __launch_bounds__(320, 1)
       const float f = KV && gw == 1 ? 1.f : scale;
       const uint32_t acc = lane_addr + C::kColAcc + (KV ? D * gw : col0);
       // KV: warpgroup 0 holds dK (accumulator 0), warpgroup 1 dV (accumulator 1)
-      __nv_bfloat16 *dst = KV && gw == 1 ? out1 + s.h * out1_head + (long long)(s.r.first + tok) * out1_row
-                           : KV          ? out0 + s.h * out0_head + (long long)(s.r.first + tok) * out0_row
-                                         : out0 + qhead * out0_head + (long long)(s.r.first + tok) * out0_row;
+      const bool second = KV && gw == 1;
+      __nv_bfloat16 *dst = second ? out1 : out0;
+      const long long to = (KV ? s.h : qhead) * (second ? out1_head : out0_head) +
+                           (long long)(s.r.first + tok) * (second ? out1_row : out0_row) + col0;
+      const int nrow = __popc(__ballot_sync(0xffffffffu, valid));   // the warp's first rows
       float4 *ps = reinterpret_cast<float4 *>(part) +
                    ((size_t)blockIdx.x * 2 + s.slot()) * ((KV ? 2 : 1) * 128 * (D / 4)) +
                    (KV ? gw * 128 * (D / 4) : 0);
@@ -485,17 +562,15 @@ __global__ void __launch_bounds__(320, 1)
         uint32_t r[32];
         tmem_ld_x32(acc + 32 * c, r);
         tmem_wait_ld();
-        if (!valid) continue;
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) v[k] = f * __uint_as_float(r[k]);
         if (whole) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            reinterpret_cast<uint4 *>(dst + col0 + 32 * c)[k] =
-                make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
-                           pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
-        } else {
+          store_rows<4>(stage, lane, nrow, to + 32 * c, dst, [&](int k) {
+            return make_uint4(pack_bf16x2(v[8 * k], v[8 * k + 1]), pack_bf16x2(v[8 * k + 2], v[8 * k + 3]),
+                              pack_bf16x2(v[8 * k + 4], v[8 * k + 5]), pack_bf16x2(v[8 * k + 6], v[8 * k + 7]));
+          });
+        } else if (valid) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             ps[(size_t)(col0 / 4 + 8 * c + k) * 128 + row] =

@@ -309,6 +309,29 @@ template <> struct Half16<__half> {
   }
 };
 
+// A warp's 32 rows of CH 16-byte chunks (lane r holds row r: chunk(k)) to global
+// memory, whole rows side by side, by way of 512 CH bytes of shared memory: a
+// store of 16 bytes a row would touch 32 lines an instruction.  `at`: this lane's
+// row as an offset into dst; the first `rows` rows are written.
+template <int CH, typename E, typename F>
+__device__ __forceinline__ void store_rows(unsigned char *stage, int lane, int rows, long long at, E *dst,
+                                           F chunk) {
+  static_assert(CH == 4 || CH == 8, "chunks of a row");
+  // 16-byte slot of chunk k of row r: eight rows of one chunk fall into eight different bank groups
+  auto slot = [&](int r, int k) { return CH == 8 ? r * 8 + (k ^ (r & 7)) : r * 4 + (k ^ ((r >> 1) & 3)); };
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < CH; ++k) *reinterpret_cast<uint4 *>(stage + 16 * slot(lane, k)) = chunk(k);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    const int r = k * (32 / CH) + lane / CH, c = lane % CH;
+    const long long a = __shfl_sync(0xffffffffu, at, r);
+    const uint4 v = *reinterpret_cast<const uint4 *>(stage + 16 * slot(r, c));
+    if (r < rows) *reinterpret_cast<uint4 *>(dst + a + c * (16 / (int)sizeof(E))) = v;
+  }
+}
+
 struct PackedOut {
   void *out;                // 16-bit rows
   long long head, row;      // strides in elements

@@ -37,7 +37,8 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
                                      const pisa_rows &dout, const float *lse, const float *out_f32, float scale,
                                      const pisa_rows &dq, const pisa_rows &dk, const pisa_rows &dv,
                                      int clear, unsigned char *ws, cudaStream_t st) {
-  using C = PackedBwdCfg<D>;
+  using Cq = PackedBwdCfg<D, false>;
+  using Ck = PackedBwdCfg<D, true>;
   const PackedBwdLayout l = packed_bwd_layout(p.T, p.Hq, D);
   float *lse2 = (float *)(ws + l.lse2), *delta = (float *)(ws + l.delta), *part = (float *)(ws + l.part);
   PackedCut *cuts = (PackedCut *)(ws + l.cuts);
@@ -55,8 +56,8 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
   PISA_TRY(map_rows(&mk, k, true, D, p.T, p.Hkv, 128));
   PISA_TRY(map_rows(&mv, v, true, D, p.T, p.Hkv, 128));
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::kSmem));
-  packed_bwd_kernel<D, false><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(
+                                 Cq::kSmem));
+  packed_bwd_kernel<D, false><<<kPackedCtas, Cq::kThreads, Cq::kSmem, st>>>(
       mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr,
       0, 0, cuts, part);
   PISA_TRY(check_launch());
@@ -67,8 +68,8 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
   PISA_TRY(map_rows(&mq, q, true, D, p.T, p.Hq, 128));
   PISA_TRY(map_rows(&mdo, dout, true, D, p.T, p.Hq, 128));
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::kSmemKv));
-  packed_bwd_kernel<D, true><<<kPackedCtas, C::kThreads, C::kSmemKv, st>>>(
+                                 Ck::kSmem));
+  packed_bwd_kernel<D, true><<<kPackedCtas, Ck::kThreads, Ck::kSmem, st>>>(
       mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dk.data, dk.head_stride, dk.row_stride,
       (__nv_bfloat16 *)dv.data, dv.head_stride, dv.row_stride, cuts, part);
   PISA_TRY(check_launch());
