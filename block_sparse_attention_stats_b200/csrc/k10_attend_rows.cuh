@@ -26,7 +26,6 @@ namespace pisa {
 
 template <int D, int R> struct RowsCfg {
   static constexpr int kConsumers = 256, kThreads = 288;
-  static constexpr int kBoxBytes = kKeyTile * 128;          // 64 columns x 128 keys
   static constexpr int kTileBytes = kKeyTile * D * 2;       // K or V of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kQBytes = R * D * 2, kPBytes = R * kKeyTile * 2;
@@ -47,29 +46,50 @@ struct PagedKV {
   int width, page_size, num_pages;
 };
 
-// Issues the copies of one tile's pages: keys key0 .. key0 + 127 of request b
-// that lie below kv, into `dst` (K, then V `v_off` bytes on).  All 32 lanes;
-// lane i brings the i-th page, whose number `page` it already holds.
-// Pages hold `rows` = min(page_size, 128) of the tile's keys each.  A page
+// Issues the copies of one tile's pages: the keys key0 .. key0 + 127 of request b
+// that lie below kv.  All 32 lanes; lane i brings the i-th page, whose number
+// `page` it already holds.  A copy brings `rows` = min(page_size, 128) keys; a page
 // number outside the cache reads as zeros (the copy's own bounds check).
+// Returns the copies to make.
 template <int D>
-__device__ __forceinline__ void issue_pages(const CUtensorMap *mk, const CUtensorMap *mv, uint32_t bar,
-                                            uint32_t dst, uint32_t v_off, int box_bytes, int key0,
-                                            int kv, int head, int page, int rows, int page_size,
-                                            int lane) {
+__device__ __forceinline__ int expect_pages(uint32_t bar, int key0, int kv, int rows, int tensors, int lane) {
   const int live = kv - key0 <= 0 ? 0 : min((kv - key0 + rows - 1) / rows, kKeyTile / rows);
-  if (lane == 0) sm100::mbar_expect_tx(bar, (uint32_t)(live * rows * D * 2 * (v_off ? 2 : 1)));
+  if (lane == 0) sm100::mbar_expect_tx(bar, (uint32_t)(live * rows * D * 2 * tensors));
   __syncwarp();
-  if (lane < live) {
-    const int row = (key0 + lane * rows) % page_size;
+  return live;
+}
+// 64-column boxes of all 128 keys one after the other, as tcgen05 reads them
+template <int D>
+__device__ __forceinline__ void issue_pages_boxed(const CUtensorMap *m, uint32_t bar, uint32_t dst, int key0,
+                                                  int kv, int head, int page, int rows, int page_size, int lane) {
+  if (lane < expect_pages<D>(bar, key0, kv, rows, 1, lane)) {
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b) {
-      const uint32_t d = dst + b * box_bytes + lane * rows * 128;
-      sm100::tma_load_4d(d, mk, bar, 64 * b, row, head, page);
-      if (v_off) sm100::tma_load_4d(d + v_off, mv, bar, 64 * b, row, head, page);
-    }
+    for (int b = 0; b < D / 64; ++b)
+      sm100::tma_load_5d(dst + b * kKeyTile * 128 + lane * rows * 128, m, bar, 0, (key0 + lane * rows) % page_size, b,
+                         head, page);
   }
   __syncwarp();
+}
+// K and V page by page, the 64-column boxes of a page together: one copy each.
+// Small copies are what small pages wait for: 48 requests of 4000 keys in pages
+// of 16 took 163 us with a copy a box.
+template <int D>
+__device__ __forceinline__ void issue_pages_whole(const CUtensorMap *mk, const CUtensorMap *mv, uint32_t bar,
+                                                  uint32_t dst, uint32_t v_off, int key0, int kv, int head,
+                                                  int page, int rows, int page_size, int lane) {
+  if (lane < expect_pages<D>(bar, key0, kv, rows, 2, lane)) {
+    const int row = (key0 + lane * rows) % page_size;
+    const uint32_t d = dst + lane * rows * D * 2;
+    sm100::tma_load_5d(d, mk, bar, 0, row, 0, head, page);
+    sm100::tma_load_5d(d + v_off, mv, bar, 0, row, 0, head, page);
+  }
+  __syncwarp();
+}
+// Byte offset of 16-byte chunk c of key `row` in a tile brought page by page
+// (1 << lg keys a page)
+template <int D> __device__ __forceinline__ uint32_t page_chunk(int row, int c, int lg) {
+  const int in = row & ((1 << lg) - 1);
+  return (uint32_t)(((row >> lg) << lg) * D * 2 + ((((c >> 3) << lg) + in) << 7) + (((c & 7) ^ (row & 7)) << 4));
 }
 
 // Page number of lane's page of the tile at key0, or -1 where there is none.
@@ -139,7 +159,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
   packed_locate<RowCost<kKeyTile>>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
   PackedWalk<RowCost<kKeyTile>> w;
   w.begin(p, *start);
-  const int page_rows = min(cache.page_size, kKeyTile);
+  const int page_rows = min(cache.page_size, kKeyTile), lg = 31 - __clz(page_rows);
 
   if (warp == 8) {
     // ======================= page loads =======================================
@@ -159,9 +179,8 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
           ok = false;
           break;
         }
-        issue_pages<D>(&tm_k, &tm_v, full(st), sbase + st * C::kStageBytes, C::kTileBytes,
-                       C::kBoxBytes, t * kKeyTile, s.r.kv, s.h, page, page_rows, cache.page_size,
-                       lane);
+        issue_pages_whole<D>(&tm_k, &tm_v, full(st), sbase + st * C::kStageBytes, C::kTileBytes,
+                             t * kKeyTile, s.r.kv, s.h, page, page_rows, cache.page_size, lane);
         page = t + 1 < s.tb
                    ? lane_page(cache, s.b, (t + 1) * kKeyTile, s.r.kv, page_rows, lane)
                    : -1;
@@ -227,8 +246,8 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
         const int z0 = max(live, 0);
         for (int e = tid; e < (kKeyTile - z0) * (D / 8); e += C::kConsumers) {
           const int row = z0 + e / (D / 8), ch = e % (D / 8);
-          *reinterpret_cast<uint4 *>(smem + st * C::kStageBytes + C::kTileBytes + (ch >> 3) * C::kBoxBytes +
-                                     row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(smem + st * C::kStageBytes + C::kTileBytes + page_chunk<D>(row, ch, lg)) =
+              make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async();
       }
@@ -244,8 +263,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
       for (int k = 0; k < D / 16; ++k) {
         uint32_t b[4];
         const int krow = 16 * warp + ((lane >> 4) << 3) + (lane & 7), kc = 2 * k + ((lane >> 3) & 1);
-        ldmatrix_x4(ks + (kc >> 3) * C::kBoxBytes + krow * 128 + (((kc & 7) ^ (krow & 7)) << 4), b[0],
-                    b[1], b[2], b[3]);
+        ldmatrix_x4(ks + page_chunk<D>(krow, kc, lg), b[0], b[1], b[2], b[3]);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           uint32_t a[4];
@@ -313,11 +331,10 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
         uint32_t b[4];
         if (NT == 2) {
           const int vrow = 16 * k + (lane & 15), vc = 2 * warp + (lane >> 4);
-          ldmatrix_x4_trans(vs + (vc >> 3) * C::kBoxBytes + vrow * 128 + (((vc & 7) ^ (vrow & 7)) << 4),
-                            b[0], b[1], b[2], b[3]);
+          ldmatrix_x4_trans(vs + page_chunk<D>(vrow, vc, lg), b[0], b[1], b[2], b[3]);
         } else {
           const int vrow = 16 * k + lane;
-          ldmatrix_x4_trans(vs + vrow * 128 + ((warp ^ (vrow & 7)) << 4), b[0], b[1], b[2], b[3]);
+          ldmatrix_x4_trans(vs + page_chunk<D>(vrow, warp, lg), b[0], b[1], b[2], b[3]);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {

@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(384, 1)
           }
           const uint32_t dst = sbase + C::kOffKV + st * C::kTileBytes;
           if constexpr (PAGED) {
-            issue_pages<D>(x ? &tm_v : &tm_k, nullptr, bar(C::kBarFull + st), dst, 0, C::kBoxBytes,
-                           t * kKeyTile, s.r.kv, s.h, page, page_rows, cache.page_size, lane);
+            issue_pages_boxed<D>(x ? &tm_v : &tm_k, bar(C::kBarFull + st), dst, t * kKeyTile, s.r.kv, s.h, page,
+                                 page_rows, cache.page_size, lane);
           } else {
             if (elect_one()) {
               mbar_expect_tx(bar(C::kBarFull + st), C::kTileBytes);

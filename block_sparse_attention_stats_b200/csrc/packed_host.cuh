@@ -58,8 +58,8 @@ inline pisa_status map16(CUtensorMap *m, const void *base, bool bf16, int rank, 
     set_last_error_text("cuTensorMapEncodeTiled is not available from the driver");
     return PISA_ERR_CUDA;
   }
-  cuuint64_t d[4], s[3];
-  cuuint32_t b[4], e[4];
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], e[5];
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     b[i] = box[i];
@@ -94,13 +94,14 @@ inline pisa_status map_query(CUtensorMap *m, const pisa_rows &r, bool bf16, int 
   return map16(m, r.data, bf16, 4, dims, st, box);
 }
 
-// rows of a page: (column, row, head, page)
+// rows of a page: (column of 64, row, 64 columns, head, page), boxes of one page's rows (128 at
+// most) and `halves` times 64 columns
 inline pisa_status map_pages(CUtensorMap *m, const pisa_pages &c, bool bf16, int d, int page_size, int H,
-                             int pages) {
-  const uint64_t dims[4] = {(uint64_t)d, (uint64_t)page_size, (uint64_t)H, (uint64_t)pages};
-  const uint64_t st[4] = {1, (uint64_t)c.row_stride, (uint64_t)c.head_stride, (uint64_t)c.page_stride};
-  const uint32_t box[4] = {64, (uint32_t)(page_size < 128 ? page_size : 128), 1, 1};
-  return map16(m, c.data, bf16, 4, dims, st, box);
+                             int pages, int halves) {
+  const uint64_t dims[5] = {64, (uint64_t)page_size, (uint64_t)d / 64, (uint64_t)H, (uint64_t)pages};
+  const uint64_t st[5] = {1, (uint64_t)c.row_stride, 64, (uint64_t)c.head_stride, (uint64_t)c.page_stride};
+  const uint32_t box[5] = {64, (uint32_t)(page_size < 128 ? page_size : 128), (uint32_t)halves, 1, 1};
+  return map16(m, c.data, bf16, 5, dims, st, box);
 }
 
 }  // namespace pisa

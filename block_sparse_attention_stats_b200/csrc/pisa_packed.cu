@@ -100,16 +100,17 @@ template <typename T, int D>
 static pisa_status run_paged(const PackedProblem &p, const PagedKV &cache, const pisa_rows &q,
                              const pisa_pages &k, const pisa_pages &v, float scale, const PackedOut &o,
                              unsigned char *ws, cudaStream_t st) {
-  CUtensorMap mk, mv;
-  PISA_TRY(map_pages(&mk, k, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages));
-  PISA_TRY(map_pages(&mv, v, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages));
   // rows of an average request (the lengths themselves are on the device; either kernel
-  // serves any of them).
+  // serves any of them)
   const long long rows = ((long long)p.T * p.G + p.B - 1) / p.B;
   const long long r = std::max<long long>(rows, p.G);
+  const bool few = r <= 32;
+  CUtensorMap mk, mv;
+  const int halves = few ? D / 64 : 1;
+  PISA_TRY(map_pages(&mk, k, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages, halves));
+  PISA_TRY(map_pages(&mv, v, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages, halves));
   if (r <= 16) return launch_rows<T, D, 16>(p, cache, q, mk, mv, scale, o, ws, st);
-  if (r <= 32) return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
-  if (r <= 64) return launch_rows<T, D, 64>(p, cache, q, mk, mv, scale, o, ws, st);
+  if (few) return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
   return launch_tc<T, D, true, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
 }
 
