@@ -96,7 +96,7 @@ template <int D> __device__ __forceinline__ uint32_t page_chunk(int row, int c, 
 __device__ __forceinline__ int lane_page(const PagedKV &c, int b, int key0, int kv, int rows, int lane) {
   const int key = key0 + lane * rows;
   if (lane >= kKeyTile / rows || key >= kv) return -1;
-  const int page = __ldg(c.table + (size_t)b * c.width + key / c.page_size);
+  const int page = sm100::ld_int(c.table + (size_t)b * c.width + key / c.page_size);
   if (page < 0 || page >= c.num_pages) {
     report_device_error(kDevErrRange);
     return -1;
@@ -122,7 +122,7 @@ template <typename T, int D, int R>
 __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
     attend_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PackedProblem p,
-                       const PagedKV cache, const T *__restrict__ q, long long q_head,
+                       const PagedKV cache, const T *q, long long q_head,
                        long long q_row, float scale, const PackedOut o, PackedCut *__restrict__ cuts,
                        float *__restrict__ part) {
   using C = RowsCfg<D, R>;
@@ -150,12 +150,13 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
     }
     fence_mbar_init();
     *abort = 0;
-    cuts[blockIdx.x].valid = 0;
   }
   if (tid == 32) {
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
+  wait_for_launches_before();
+  if (tid == 0) cuts[blockIdx.x].valid = 0;
   packed_locate<RowCost<kKeyTile>>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
   PackedWalk<RowCost<kKeyTile>> w;
   w.begin(p, *start);
@@ -205,8 +206,8 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
       const int row = e / (D / 8), ch = e % (D / 8);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (row < rows)
-        v = *reinterpret_cast<const uint4 *>(q + (long long)(s.h * p.G + row % p.G) * q_head +
-                                             (long long)(s.r.first + tok0 + row / p.G) * q_row + 8 * ch);
+        v = __ldcg(reinterpret_cast<const uint4 *>(q + (long long)(s.h * p.G + row % p.G) * q_head +
+                                                   (long long)(s.r.first + tok0 + row / p.G) * q_row + 8 * ch));
       *reinterpret_cast<uint4 *>(smem + C::kOffQ + SwizzledTile<D>::offset(row, 8 * ch)) = v;
     }
     // keys each of this thread's rows sees: positions below lim

@@ -203,7 +203,6 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(bar(C::kBarTeardown), 1);
     fence_mbar_init();
     *abort = 0;
-    cuts[blockIdx.x].valid = 0;
   }
   if (tid == 32) {
     prefetch_tmap(&tm_q);
@@ -218,6 +217,8 @@ __global__ void __launch_bounds__(384, 1)
   }
   fence_proxy_async();
   tc_fence_before();
+  wait_for_launches_before();
+  if (tid == 0) cuts[blockIdx.x].valid = 0;
   packed_locate<RowCost<kKeyTile>>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;

@@ -40,20 +40,23 @@ namespace pisa {
 // lse2 = lse log2 e and Delta, [Hq, T]: one warp a row
 template <int D>
 __global__ void __launch_bounds__(256)
-    packed_delta_kernel(const __nv_bfloat16 *__restrict__ dout, long long head_stride, long long row_stride,
-                        const float *__restrict__ out, const float *__restrict__ lse, int Hq, int T,
-                        const int32_t *__restrict__ cu, int B, float *__restrict__ lse2,
+    packed_delta_kernel(const __nv_bfloat16 *dout, long long head_stride, long long row_stride,
+                        const float *out, const float *lse, int Hq, int T,
+                        const int32_t *cu, int B, float *__restrict__ lse2,
                         float *__restrict__ delta) {
+  sm100::allow_next_launch();
+  sm100::wait_for_launches_before();
   const int lane = threadIdx.x & 31;
-  const int end = min(max(__ldg(cu + B), 0), T);      // rows behind the last sequence are not read
+  const int end = min(max(sm100::ld_int(cu + B), 0), T);      // rows behind the last sequence are not read
   const long long rows = (long long)Hq * T;
   for (long long r = (blockIdx.x * 256ll + threadIdx.x) >> 5; r < rows; r += gridDim.x * 8ll) {
     const int h = (int)(r / T), t = (int)(r % T);
     if (t >= end) continue;
     float s = 0.f;
     if (lane < D / 4) {
-      const float4 o = reinterpret_cast<const float4 *>(out + r * D)[lane];
-      const uint2 g = *reinterpret_cast<const uint2 *>(dout + h * head_stride + t * row_stride + 4 * lane);
+      const float4 o = __ldcg(reinterpret_cast<const float4 *>(out + r * D) + lane);
+      const uint2 g =
+          __ldcg(reinterpret_cast<const uint2 *>(dout + h * head_stride + t * row_stride + 4 * lane));
       const float2 a = Half16<__nv_bfloat16>::unpack(g.x), b = Half16<__nv_bfloat16>::unpack(g.y);
       s = fmaf(o.x, a.x, fmaf(o.y, a.y, fmaf(o.z, b.x, o.w * b.y)));
     }
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(256)
     for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
     if (lane == 0) {
       delta[r] = s;
-      lse2[r] = lse[r] * kLog2e;
+      lse2[r] = __ldcg(lse + r) * kLog2e;
     }
   }
 }
@@ -95,8 +98,8 @@ template <int D, bool KV>
 __global__ void __launch_bounds__(320, 1)
     packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const PackedProblem p, float scale, const float *__restrict__ lse2,
-                      const float *__restrict__ delta, __nv_bfloat16 *__restrict__ out0,
+                      const PackedProblem p, float scale, const float *lse2, const float *delta,
+                      __nv_bfloat16 *__restrict__ out0,
                       long long out0_head, long long out0_row, __nv_bfloat16 *__restrict__ out1,
                       long long out1_head, long long out1_row, PackedCut *__restrict__ cuts,
                       float *__restrict__ part) {
@@ -133,7 +136,6 @@ __global__ void __launch_bounds__(320, 1)
     }
     fence_mbar_init();
     *abort = 0;
-    cuts[blockIdx.x].valid = 0;
   }
   if (tid == 32) {
     prefetch_tmap(&tm_q);
@@ -142,6 +144,8 @@ __global__ void __launch_bounds__(320, 1)
     prefetch_tmap(&tm_v);
   }
   tc_fence_before();
+  wait_for_launches_before();
+  if (tid == 0) cuts[blockIdx.x].valid = 0;
   packed_locate<Cost>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -219,8 +223,8 @@ __global__ void __launch_bounds__(320, 1)
             const int r = lane + 32 * k;
             const bool in = row0 + r < s.r.n;
             const size_t at = (size_t)head * p.T + s.r.first + row0 + r;
-            lv[k] = in ? lse2[at] : INFINITY;     // exp2(x - inf) = 0: a row that is not there
-            dv[k] = in ? delta[at] : 0.f;
+            lv[k] = in ? __ldcg(lse2 + at) : INFINITY;     // exp2(x - inf) = 0: a row that is not there
+            dv[k] = in ? __ldcg(delta + at) : 0.f;
           }
         }
 #pragma unroll
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(320, 1)
       const bool valid = tok < s.r.n && row < sub_rows;
       const int qhead = s.h * p.G + row % p.G;
       const size_t hr = (size_t)qhead * p.T + s.r.first + tok;
-      const float lrow = !KV && valid ? lse2[hr] : 0.f, drow = !KV && valid ? delta[hr] : 0.f;
+      const float lrow = !KV && valid ? __ldcg(lse2 + hr) : 0.f, drow = !KV && valid ? __ldcg(delta + hr) : 0.f;
       for (int t = s.ta; t < s.tb; ++t, ++u) {
         const int row0 = tile_at(s, t, g);
         const float *ls = vec + (u % C::kVecs) * 256 + 64 * gw, *dl = ls + 128;
@@ -596,16 +600,18 @@ __global__ void __launch_bounds__(320, 1)
 // Joins the partial sums of the unit that CTA blockIdx.x's range cuts, in
 // ascending CTA order.  blockIdx.z: dk or dv (KV).
 template <int D, bool KV>
-__global__ void __launch_bounds__(256)
-    packed_sum_kernel(const PackedProblem p, const PackedCut *__restrict__ cuts, const float *__restrict__ part,
+__global__ void __launch_bounds__(128)
+    packed_sum_kernel(const PackedProblem p, const PackedCut *cuts, const float *part,
                       __nv_bfloat16 *__restrict__ out0, long long out0_head, long long out0_row,
                       __nv_bfloat16 *__restrict__ out1, long long out1_head, long long out1_row, int clear) {
+  sm100::allow_next_launch();
+  sm100::wait_for_launches_before();
   if (clear)
     clear_tail<D>(p, KV ? p.Hkv : p.Hq, blockIdx.z ? out1 : out0, blockIdx.z ? out1_head : out0_head,
                   blockIdx.z ? out1_row : out0_row,
                   ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
                   (long long)gridDim.x * gridDim.y * blockDim.x);
-  const PackedCut cut = cuts[blockIdx.x];
+  const PackedCut cut = packed_cut_at(cuts, blockIdx.x);
   if (!cut.valid) return;
   const PackedRequest r = packed_request(p, cut.b);
   const int per = KV ? 128 : p.tq, g = KV ? 1 : p.G, tok0 = cut.rt * per;
@@ -615,18 +621,38 @@ __global__ void __launch_bounds__(256)
   const float4 *base = reinterpret_cast<const float4 *>(part) + blockIdx.z * (128 * (D / 4));
   __nv_bfloat16 *out = blockIdx.z ? out1 : out0;
   const long long hs = blockIdx.z ? out1_head : out0_head, rs = blockIdx.z ? out1_row : out0_row;
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 4); e += gridDim.y * blockDim.x) {
-    const int row = e / (D / 4), c4 = e % (D / 4);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-      const float4 x = base[((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kSlot + (size_t)c4 * 128 + row];
-      a.x += x.x;
-      a.y += x.y;
-      a.z += x.z;
-      a.w += x.w;
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 16); e += gridDim.y * blockDim.x) {
+    const int row = e % rows, c16 = e / rows;
+    float acc[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float4 x[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(i0 + k, n - 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[k][j] = __ldcg(base + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * kSlot + (size_t)(4 * c16 + j) * 128 + row);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i0 + k >= n) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[4 * j] += x[k][j].x;
+          acc[4 * j + 1] += x[k][j].y;
+          acc[4 * j + 2] += x[k][j].z;
+          acc[4 * j + 3] += x[k][j].w;
+        }
+      }
     }
-    const long long at = (cut.h * g + row % g) * hs + (long long)(r.first + tok0 + row / g) * rs + 4 * c4;
-    *reinterpret_cast<uint2 *>(out + at) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    const long long at = (cut.h * g + row % g) * hs + (long long)(r.first + tok0 + row / g) * rs + 16 * c16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      reinterpret_cast<uint4 *>(out + at)[j] =
+          make_uint4(pack_bf16x2(acc[8 * j], acc[8 * j + 1]), pack_bf16x2(acc[8 * j + 2], acc[8 * j + 3]),
+                     pack_bf16x2(acc[8 * j + 4], acc[8 * j + 5]), pack_bf16x2(acc[8 * j + 6], acc[8 * j + 7]));
   }
 }
 

@@ -14,7 +14,7 @@
 // table, so no CTA waits for another's table entries.
 #pragma once
 
-#include "pisa_common.cuh"
+#include "packed_primitives.cuh"
 
 namespace pisa {
 
@@ -37,13 +37,15 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
   int *cu = plan_sm, *need = plan_sm + p.B + 1;   // exclusive prefix sums
   __shared__ long long wsum[2][kPlanThreads / 32];
   __shared__ int wbad[kPlanThreads / 32];
+  sm100::allow_next_launch();
+  sm100::wait_for_launches_before();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long sn = 0, sp = 0;
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
-    const long long past = p.past[b], fresh = p.fresh[b];
+    const long long past = sm100::ld_int(p.past + b), fresh = sm100::ld_int(p.fresh + b);
     bad = bad || past < 0 || fresh < 0 || past + fresh > 0x7fffffffll;
     const long long want = (past + fresh + p.page_size - 1) / p.page_size;
     bad = bad || want > p.width;
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
     tp += wsum[1][w];
     anybad |= wbad[w];
   }
-  const int nf = *p.num_free;
+  const int nf = sm100::ld_int(p.num_free);
   // all or nothing: a step that does not fit changes no table and gives no slot
   const bool ok = !anybad && tn <= p.T && nf >= 0 && nf <= p.free_cap && tp <= nf;
   const int gid = blockIdx.x * kPlanThreads + tid, gsz = gridDim.x * kPlanThreads;
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
     }
     for (int b = gid; b < p.B; b += gsz) {
       p.cu[b] = 0;
-      p.kv_lens[b] = p.past[b];
+      p.kv_lens[b] = sm100::ld_int(p.past + b);
     }
     for (int r = gid; r < p.T; r += gsz) p.slots[r] = -1;
     return;
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
   for (int b = b0; b < b1; ++b) {
     cu[b] = (int)an;
     need[b] = (int)ap;
-    const int past = p.past[b], fresh = p.fresh[b];
+    const int past = sm100::ld_int(p.past + b), fresh = sm100::ld_int(p.fresh + b);
     an += fresh;
     ap += (past + (long long)fresh + p.page_size - 1) / p.page_size -
           (past + (long long)p.page_size - 1) / p.page_size;
@@ -121,11 +123,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
     long long slot = -1;
     if (r < (int)tn) {
       const int b = find(cu, r);
-      const long long pos = (long long)p.past[b] + r - cu[b];
-      const int have = (int)(((long long)p.past[b] + p.page_size - 1) / p.page_size);
+      const long long past = sm100::ld_int(p.past + b), pos = past + r - cu[b];
+      const int have = (int)((past + p.page_size - 1) / p.page_size);
       const int at = (int)(pos / p.page_size);
-      const int page = at < have ? p.table[(size_t)b * p.width + at]
-                                 : p.free_pages[nf - 1 - (need[b] + at - have)];
+      const int page = at < have ? sm100::ld_int(p.table + (size_t)b * p.width + at)
+                                 : sm100::ld_int(p.free_pages + (nf - 1 - (need[b] + at - have)));
       if (page >= 0) slot = (long long)page * p.page_size + pos % p.page_size;
       else report_device_error(kDevErrRange);
     }
@@ -133,12 +135,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
   }
   for (int n = gid; n < (int)tp; n += gsz) {
     const int b = find(need, n);
-    const int have = (int)(((long long)p.past[b] + p.page_size - 1) / p.page_size);
-    p.table[(size_t)b * p.width + have + n - need[b]] = p.free_pages[nf - 1 - n];
+    const int have = (int)(((long long)sm100::ld_int(p.past + b) + p.page_size - 1) / p.page_size);
+    p.table[(size_t)b * p.width + have + n - need[b]] = sm100::ld_int(p.free_pages + (nf - 1 - n));
   }
   for (int b = gid; b <= p.B; b += gsz) {
     p.cu[b] = cu[b];
-    if (b < p.B) p.kv_lens[b] = p.past[b] + p.fresh[b];
+    if (b < p.B) p.kv_lens[b] = sm100::ld_int(p.past + b) + sm100::ld_int(p.fresh + b);
   }
   if (gid == 0) *p.num_free_out = nf - (int)tp;
 }
@@ -161,6 +163,8 @@ constexpr int kWriteThreads = 256, kWriteRows = 4;
 
 // CH: 16-byte chunks of a row (d / 8).  blockIdx.y: head, blockIdx.z: k or v.
 template <int CH> __global__ void __launch_bounds__(kWriteThreads) page_write_kernel(const PageWrite p) {
+  sm100::allow_next_launch();
+  sm100::wait_for_launches_before();
   constexpr int kPer = kWriteThreads / CH;   // rows that the CTA's threads cover at once
   const int x = blockIdx.z, h = blockIdx.y;
   const int c = threadIdx.x % CH, r0 = threadIdx.x / CH;
@@ -173,8 +177,8 @@ template <int CH> __global__ void __launch_bounds__(kWriteThreads) page_write_ke
 #pragma unroll
     for (int i = 0; i < kWriteRows; ++i) {
       const long long t = t0 + i * kPer + r0;
-      slot[i] = t < p.T ? p.slots[t] : -1;
-      if (t < p.T) v[i] = __ldcs(reinterpret_cast<const uint4 *>(src + t * p.src_row[x]));
+      slot[i] = t < p.T ? __ldcg(reinterpret_cast<const long long *>(p.slots) + t) : -1;
+      if (t < p.T) v[i] = __ldcg(reinterpret_cast<const uint4 *>(src + t * p.src_row[x]));
     }
 #pragma unroll
     for (int i = 0; i < kWriteRows; ++i) {

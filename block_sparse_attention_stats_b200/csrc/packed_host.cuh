@@ -32,6 +32,26 @@ constexpr int kPackedCtas = 148;
     }                                          \
   } while (0)
 
+// Launches a kernel that may be set up while the kernel before it on the stream still runs (it
+// waits for that one by itself, see wait_for_launches_before): between the short kernels of a
+// decode step the gap is most of the time.
+template <typename... P, typename... A>
+inline pisa_status launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st,
+                                const A &...args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  PISA_CUDA(cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...));
+  return PISA_OK;
+}
+
 inline bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // [H][T] rows of d elements at the given strides: 16-byte aligned, rows of one

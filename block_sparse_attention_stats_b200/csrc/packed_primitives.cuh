@@ -32,6 +32,19 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+// Programmatic dependent launch: the next kernel of the stream may be set up from here on; and
+// wait until the kernels before this one are complete and their writes are seen.  Every kernel
+// that launch_after starts waits before it touches global memory, and reads what kernels before
+// it may have written with ld_int (an ordinary load: the wait makes their writes visible to it) or
+// __ldcg, never through the read-only path: it has been running while they wrote.
+__device__ __forceinline__ void allow_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_launches_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ int ld_int(const int32_t *p) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // generic-proxy writes to shared memory, made visible to the tensor cores and TMA
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -19,7 +19,7 @@
 
 #include <math.h>
 
-#include "pisa_common.cuh"
+#include "packed_primitives.cuh"
 
 namespace pisa {
 
@@ -45,20 +45,20 @@ struct PackedRequest {
 // [0, T) and positions inside [0, max_kv].
 __device__ __forceinline__ PackedRequest packed_request(const PackedProblem &p, int b) {
   PackedRequest r;
-  const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
+  const int lo = sm100::ld_int(p.cu + b), hi = sm100::ld_int(p.cu + b + 1);
   r.first = min(max(lo, 0), p.T);
   r.n = max(min(hi, p.T) - r.first, 0);
   r.kv = r.n;
-  if (p.kv_lens) r.kv = min(max(__ldg(p.kv_lens + b), 0), p.max_kv);
+  if (p.kv_lens) r.kv = min(max(sm100::ld_int(p.kv_lens + b), 0), p.max_kv);
   r.past = r.kv - r.n;
   return r;
 }
 
 __device__ __forceinline__ bool packed_request_malformed(const PackedProblem &p, int b) {
-  const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
+  const int lo = sm100::ld_int(p.cu + b), hi = sm100::ld_int(p.cu + b + 1);
   bool bad = lo < 0 || hi < lo || hi > p.T;
   if (p.kv_lens) {
-    const int kv = __ldg(p.kv_lens + b);
+    const int kv = sm100::ld_int(p.kv_lens + b);
     bad = bad || kv < 0 || kv > p.max_kv;
   }
   return bad;
@@ -274,6 +274,11 @@ struct PackedCut {
   int valid, b, rt, h, last;   // last: the CTA that holds the unit's last tile
 };
 
+__device__ __forceinline__ PackedCut packed_cut_at(const PackedCut *cuts, int c) {
+  const int *x = reinterpret_cast<const int *>(cuts + c);
+  return PackedCut{__ldcg(x), __ldcg(x + 1), __ldcg(x + 2), __ldcg(x + 3), __ldcg(x + 4)};
+}
+
 __device__ __forceinline__ PackedCut packed_cut(const PackedStart &st, const PackedSegment &s) {
   PackedCut c;
   c.valid = 1;
@@ -344,7 +349,7 @@ struct PackedOut {
 template <int D>
 __device__ __forceinline__ void clear_tail(const PackedProblem &p, int H, void *out, long long head_stride,
                                            long long row_stride, long long me, long long threads) {
-  const int end = min(max(__ldg(p.cu + p.B), 0), p.T);
+  const int end = min(max(sm100::ld_int(p.cu + p.B), 0), p.T);
   const long long n = (long long)H * (p.T - end) * (D / 8);
   for (long long e = me; e < n; e += threads) {
     const long long r = e / (D / 8);
@@ -356,52 +361,82 @@ __device__ __forceinline__ void clear_tail(const PackedProblem &p, int H, void *
 
 // Joins the partials of the unit that CTA blockIdx.x's range cuts:
 //   m = max_i m_i,  l = sum_i l_i 2^(m_i - m),  o = sum_i O_i 2^(m_i - m) / l
-// (m in units of log2).  One thread per (row, four columns).
+// (m in units of log2).  One thread per (row, 16 columns): neighbouring threads
+// read neighbouring rows.
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
-    packed_combine_kernel(const PackedProblem p, const PackedCut *__restrict__ cuts,
-                          const float *__restrict__ part, int R, const PackedOut o, int clear) {
+__global__ void __launch_bounds__(128)
+    packed_combine_kernel(const PackedProblem p, const PackedCut *cuts,
+                          const float *part, int R, const PackedOut o, int clear) {
+  sm100::wait_for_launches_before();
   if (clear)
     clear_tail<D>(p, p.Hq, o.out, o.head, o.row,
                   ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
                   (long long)gridDim.x * gridDim.y * blockDim.x);
-  const PackedCut cut = cuts[blockIdx.x];
+  const PackedCut cut = packed_cut_at(cuts, blockIdx.x);
   if (!cut.valid) return;
   const PackedRequest r = packed_request(p, cut.b);
   const int tok0 = cut.rt * p.tq, rows = min(r.n - tok0, p.tq) * p.G;
   const size_t slot = packed_slot_floats<D>(R);
   const int c0 = blockIdx.x, n = cut.last - c0 + 1;
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 4); e += gridDim.y * blockDim.x) {
-    const int row = e / (D / 4), c4 = e % (D / 4);
-    // partial i: slot 1 of the first CTA, slot 0 of the later ones
-    auto at = [&](int i) { return part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot; };
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[row]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-      const float *s = at(i);
-      const float f = exp2f(s[row] - base);
-      if (f == 0.f) continue;   // no weight (and, of a tile without keys, no output either)
-      const float4 x = reinterpret_cast<const float4 *>(s + 2 * R)[(size_t)c4 * R + row];
-      l = fmaf(f, s[R + row], l);
-      acc.x = fmaf(f, x.x, acc.x);
-      acc.y = fmaf(f, x.y, acc.y);
-      acc.z = fmaf(f, x.z, acc.z);
-      acc.w = fmaf(f, x.w, acc.w);
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 16); e += gridDim.y * blockDim.x) {
+    const int row = e % rows, c16 = e / rows;
+    float base = -INFINITY, l = 0.f, acc[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
+    // four partials at a time: their loads are in flight together
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float m[4], ls[4];
+      float4 x[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = min(i0 + k, n - 1);
+        // partial i: slot 1 of the first CTA, slot 0 of the later ones
+        const float *s = part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot;
+        m[k] = __ldcg(s + row);
+        ls[k] = __ldcg(s + R + row);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[k][j] = __ldcg(reinterpret_cast<const float4 *>(s + 2 * R) + (size_t)(4 * c16 + j) * R + row);
+        if (i0 + k >= n) m[k] = -INFINITY;
+      }
+      const float top = fmaxf(fmaxf(base, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+      const float from = top == -INFINITY ? 0.f : top;
+      const float f0 = exp2f(base - from);
+      l *= f0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[j] *= f0;
+      base = top;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = exp2f(m[k] - from);
+        if (f == 0.f) continue;   // no weight (and, of a tile without keys, no output either)
+        l = fmaf(f, ls[k], l);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[4 * j] = fmaf(f, x[k][j].x, acc[4 * j]);
+          acc[4 * j + 1] = fmaf(f, x[k][j].y, acc[4 * j + 1]);
+          acc[4 * j + 2] = fmaf(f, x[k][j].z, acc[4 * j + 2]);
+          acc[4 * j + 3] = fmaf(f, x[k][j].w, acc[4 * j + 3]);
+        }
+      }
     }
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // a row without keys is zero; NaN stays
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] *= inv;
     const int token = r.first + tok0 + row / p.G, head = cut.h * p.G + row % p.G;
-    uint2 w;
-    w.x = Half16<T>::pack(acc.x * inv, acc.y * inv);
-    w.y = Half16<T>::pack(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2 *>(reinterpret_cast<T *>(o.out) + head * o.head + token * o.row + 4 * c4) = w;
+    uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(o.out) + head * o.head + token * o.row + 16 * c16);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      dst[j] = make_uint4(Half16<T>::pack(acc[8 * j], acc[8 * j + 1]), Half16<T>::pack(acc[8 * j + 2], acc[8 * j + 3]),
+                          Half16<T>::pack(acc[8 * j + 4], acc[8 * j + 5]),
+                          Half16<T>::pack(acc[8 * j + 6], acc[8 * j + 7]));
     const size_t hr = (size_t)head * p.T + token;
     if (o.f32)
-      reinterpret_cast<float4 *>(o.f32 + hr * D)[c4] =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (o.lse && c4 == 0) o.lse[hr] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        reinterpret_cast<float4 *>(o.f32 + hr * D + 16 * c16)[j] =
+            make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+    if (o.lse && c16 == 0) o.lse[hr] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
   }
 }
 

@@ -36,10 +36,8 @@ static PackedScratch packed_scratch(int d, int rows) {
 template <typename T, int D>
 static pisa_status launch_combine(const PackedProblem &p, const PackedCut *cuts, const float *part, int R,
                                   const PackedOut &o, int clear, cudaStream_t st) {
-  // a few hundred rows by D / 4 threads each are joined per cut unit
-  const int y = std::max(1, std::min(16, R * (D / 4) / 256));
-  packed_combine_kernel<T, D><<<dim3(kPackedCtas, y), 256, 0, st>>>(p, cuts, part, R, o, clear);
-  return check_launch();
+  const int y = std::max(1, R * (D / 16) / 128);
+  return launch_after(packed_combine_kernel<T, D>, dim3(kPackedCtas, y), 128, 0, st, p, cuts, part, R, o, clear);
 }
 
 template <typename T, int D, bool PAGED, bool ROUNDED>
@@ -60,9 +58,8 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
   float *part = (float *)(ws + s.part);
   PISA_CUDA(cudaFuncSetAttribute(attend_tc_kernel<T, D, PAGED, ROUNDED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem));
-  attend_tc_kernel<T, D, PAGED, ROUNDED><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(mq, mk, mv, p, cache, scale, o,
-                                                                            cuts, part);
-  PISA_TRY(check_launch());
+  PISA_TRY(launch_after(attend_tc_kernel<T, D, PAGED, ROUNDED>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, mq, mk, mv, p, cache, scale, o,
+                                                                            cuts, part));
   return launch_combine<T, D>(p, cuts, part, C::kRows, o, clear, st);
 }
 
@@ -79,9 +76,8 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
   float *part = (float *)(ws + s.part);
   PISA_CUDA(cudaFuncSetAttribute(attend_rows_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem));
-  attend_rows_kernel<T, D, R><<<kPackedCtas, C::kThreads, C::kSmem, st>>>(
-      mk, mv, p, cache, (const T *)q.data, q.head_stride, q.row_stride, scale, o, cuts, part);
-  PISA_TRY(check_launch());
+  PISA_TRY(launch_after(attend_rows_kernel<T, D, R>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, 
+      mk, mv, p, cache, (const T *)q.data, q.head_stride, q.row_stride, scale, o, cuts, part));
   return launch_combine<T, D>(p, cuts, part, R, o, 0, st);
 }
 
@@ -274,8 +270,7 @@ pisa_status pisa_page_plan(const pisa_page_step *step, pisa_stream_t stream) {
                                  2 * (kPlanMaxB + 1) * (int)sizeof(int)));
   const int work = std::max(p.T, p.B + 1);
   const int grid = std::max(1, std::min(ceil_div(work, kPlanThreads), kPackedCtas));
-  page_plan_kernel<<<grid, kPlanThreads, smem, (cudaStream_t)stream>>>(p);
-  return check_launch();
+  return launch_after(page_plan_kernel, dim3(grid), kPlanThreads, smem, (cudaStream_t)stream, p);
 }
 
 pisa_status pisa_page_write(pisa_rows k, pisa_rows v, pisa_dtype dtype, const int64_t *slots, int T, int Hkv,
@@ -314,11 +309,8 @@ pisa_status pisa_page_write(pisa_rows k, pisa_rows v, pisa_dtype dtype, const in
   w.num_slots = (long long)num_pages * page_size;
   const int per = kWriteThreads / (d / 8) * kWriteRows;
   const dim3 grid(std::min(ceil_div(T, per), 65535), Hkv, 2);
-  if (d == 128)
-    page_write_kernel<16><<<grid, kWriteThreads, 0, (cudaStream_t)stream>>>(w);
-  else
-    page_write_kernel<8><<<grid, kWriteThreads, 0, (cudaStream_t)stream>>>(w);
-  return check_launch();
+  if (d == 128) return launch_after(page_write_kernel<16>, grid, kWriteThreads, 0, (cudaStream_t)stream, w);
+  return launch_after(page_write_kernel<8>, grid, kWriteThreads, 0, (cudaStream_t)stream, w);
 }
 
 pisa_status pisa_paged_step(const pisa_page_step *step, pisa_rows q, pisa_rows k, pisa_rows v,

@@ -43,10 +43,9 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
   float *lse2 = (float *)(ws + l.lse2), *delta = (float *)(ws + l.delta), *part = (float *)(ws + l.part);
   PackedCut *cuts = (PackedCut *)(ws + l.cuts);
   const long long rows = (long long)p.Hq * p.T;
-  packed_delta_kernel<D><<<(unsigned)std::min<long long>((rows + 7) / 8, 148 * 8), 256, 0, st>>>(
+  PISA_TRY(launch_after(packed_delta_kernel<D>, dim3((unsigned)std::min<long long>((rows + 7) / 8, 148 * 8)), 256, 0, st, 
       (const __nv_bfloat16 *)dout.data, dout.head_stride, dout.row_stride, out_f32, lse, p.Hq, p.T, p.cu, p.B,
-      lse2, delta);
-  PISA_TRY(check_launch());
+      lse2, delta));
   p.tq = 128 / p.G;
   p.min_tiles = 4;
   p.unit_cost = 2;
@@ -57,26 +56,22 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
   PISA_TRY(map_rows(&mv, v, true, D, p.T, p.Hkv, 128));
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Cq::kSmem));
-  packed_bwd_kernel<D, false><<<kPackedCtas, Cq::kThreads, Cq::kSmem, st>>>(
+  PISA_TRY(launch_after(packed_bwd_kernel<D, false>, dim3(kPackedCtas), Cq::kThreads, Cq::kSmem, st, 
       mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr,
-      0, 0, cuts, part);
-  PISA_TRY(check_launch());
-  packed_sum_kernel<D, false><<<dim3(kPackedCtas, 8), 256, 0, st>>>(
-      p, cuts, part, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr, 0, 0, clear);
-  PISA_TRY(check_launch());
+      0, 0, cuts, part));
+  PISA_TRY(launch_after(packed_sum_kernel<D, false>, dim3(kPackedCtas, D / 16), 128, 0, st, 
+      p, cuts, part, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr, 0, 0, clear));
   // dk, dv: Q and dout one head at a time
   PISA_TRY(map_rows(&mq, q, true, D, p.T, p.Hq, 128));
   PISA_TRY(map_rows(&mdo, dout, true, D, p.T, p.Hq, 128));
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Ck::kSmem));
-  packed_bwd_kernel<D, true><<<kPackedCtas, Ck::kThreads, Ck::kSmem, st>>>(
+  PISA_TRY(launch_after(packed_bwd_kernel<D, true>, dim3(kPackedCtas), Ck::kThreads, Ck::kSmem, st, 
       mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dk.data, dk.head_stride, dk.row_stride,
-      (__nv_bfloat16 *)dv.data, dv.head_stride, dv.row_stride, cuts, part);
-  PISA_TRY(check_launch());
-  packed_sum_kernel<D, true><<<dim3(kPackedCtas, 8, 2), 256, 0, st>>>(
+      (__nv_bfloat16 *)dv.data, dv.head_stride, dv.row_stride, cuts, part));
+  return launch_after(packed_sum_kernel<D, true>, dim3(kPackedCtas, D / 16, 2), 128, 0, st, 
       p, cuts, part, (__nv_bfloat16 *)dk.data, dk.head_stride, dk.row_stride, (__nv_bfloat16 *)dv.data,
       dv.head_stride, dv.row_stride, clear);
-  return check_launch();
 }
 
 }  // namespace pisa
