@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
   }
   wait_for_launches_before();
   if (tid == 0) cuts[blockIdx.x].valid = 0;
-  packed_locate<RowCost<kKeyTile>>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
-  PackedWalk<RowCost<kKeyTile>> w;
+  packed_locate<RowCost>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
+  PackedWalk<RowCost> w;
   w.begin(p, *start);
   const int page_rows = min(cache.page_size, kKeyTile), lg = 31 - __clz(page_rows);
 
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
           }
         }
       }
-    if (!whole && s.ta == 0 && tid == 0) cuts[blockIdx.x] = packed_cut(*start, s);
+    if (!whole && s.ta == 0 && tid == 0) cuts[blockIdx.x] = packed_cut(p, *start, s, gridDim.x);
   }
 }
 

@@ -69,7 +69,7 @@ __device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedS
   SubTile x;
   const int tok = s.rt * p.tq + i * tq1;
   x.rows = max(min(s.r.n - tok, tq1), 0) * p.G;
-  x.nt = x.rows == 0 ? 0 : RowCost<kKeyTile>::tiles(p, s.r.n, s.r.kv, tq1, 2 * s.rt + i);
+  x.nt = x.rows == 0 ? 0 : packed_tiles(RowCost::length(p, s.r.n, s.r.kv, tq1, 2 * s.rt + i));
   return x;
 }
 
@@ -94,10 +94,19 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
   tmem_ld_x32(s_addr + 64, reinterpret_cast<uint32_t(&)[32]>(r[64]));
   tmem_ld_x32(s_addr + 96, reinterpret_cast<uint32_t(&)[32]>(r[96]));
   auto sv = [&](int c) -> float { return __uint_as_float(r[c]); };
+  // bit c of word w: column 32 w + c is visible
   const bool masked = __any_sync(0xffffffffu, seen < kKeyTile);
+  auto word = [&](int w) -> uint32_t {
+    const int n = seen - 32 * w;
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  };
   if (masked) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) r[c] = c < seen ? r[c] : 0xff800000u;
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t m = word(w);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) r[32 * w + c] = (m >> c) & 1u ? r[32 * w + c] : 0xff800000u;
+    }
   }
   float mx[8];
 #pragma unroll
@@ -111,7 +120,11 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
   tmem_wait_ld();
   if (masked) {
 #pragma unroll
-    for (int c = 64; c < 128; ++c) r[c] = c < seen ? r[c] : 0xff800000u;
+    for (int w = 2; w < 4; ++w) {
+      const uint32_t m = word(w);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) r[32 * w + c] = (m >> c) & 1u ? r[32 * w + c] : 0xff800000u;
+    }
   }
 #pragma unroll
   for (int k = 64; k < 128; k += 16)
@@ -219,10 +232,10 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_before();
   wait_for_launches_before();
   if (tid == 0) cuts[blockIdx.x].valid = 0;
-  packed_locate<RowCost<kKeyTile>>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
+  packed_locate<RowCost>(p, blockIdx.x, gridDim.x, tid, C::kThreads, wsum, start);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  PackedWalk<RowCost<kKeyTile>> w;
+  PackedWalk<RowCost> w;
   w.begin(p, *start);
 
   auto uwait = [&](uint32_t b_addr, uint32_t parity) -> bool {
@@ -355,8 +368,6 @@ __global__ void __launch_bounds__(384, 1)
       for (int t = cur.ta; t < cur.tb; ++t, slot += 2) {
         // after P V of this tile comes S of the next one, which may be the next unit's first
         const bool last = t + 1 == cur.tb;
-        if (last) have_n = take(nxt);
-        const bool more = !last || have_n;
         bool have_v = false, have_k = false;
 #pragma unroll
         for (int i = 0; ok && i < 2; ++i) {
@@ -417,10 +428,10 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             ++np[i];
           }
-          if (last ? (have_n && nxt.ta < nxt.nt[i]) : t + 1 < nt) {
+          if (t + 1 < nt) {
             if (!have_k) {
               have_k = true;
-              if ((last && !uwait(bar(C::kBarQFull), (seg + 1) & 1)) || !full(slot + 2)) {
+              if (!full(slot + 2)) {
                 ok = false;
                 break;
               }
@@ -431,6 +442,18 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (!ok) break;
         commit(C::kBarEmpty + (slot + 1) % C::kStages);
+        // (after P V of both subtiles: the next unit's Q may still be on its way)
+        if (last) have_n = take(nxt);
+        const bool more = !last || have_n;
+        if (last && have_n) {
+          if (!uwait(bar(C::kBarQFull), (seg + 1) & 1) || !full(slot + 2)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (nxt.ta < nxt.nt[0]) issue_s(0, slot + 2);
+          if (nxt.ta < nxt.nt[1]) issue_s(1, slot + 2);
+        }
         if (more) {
           commit(C::kBarEmpty + (slot + 2) % C::kStages);
           if (last ? nxt.ta + 1 == nxt.tb : t + 2 == cur.tb) commit(C::kBarQEmpty);
@@ -506,44 +529,39 @@ __global__ void __launch_bounds__(384, 1)
         // rows of the warp that are stored, and where each goes
         const int nrow = min(max(x.rows - sp * 32, 0), 32);
         const long long at = (long long)head * o.head + (long long)token * o.row;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t ov[64];
-          tmem_ld_x32(o_addr + 64 * c, reinterpret_cast<uint32_t(&)[32]>(ov[0]));
-          tmem_ld_x32(o_addr + 64 * c + 32, reinterpret_cast<uint32_t(&)[32]>(ov[32]));
+        // (a loop, not unrolled: units of a few tiles come back to this code often enough that its
+        // length is paid for in instruction fetches)
+        float4 *ps = reinterpret_cast<float4 *>(slot + 2 * C::kRows) + prow;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld_x32(o_addr + 32 * c, ov);
           tmem_wait_ld();
+          if (c + 1 == D / 32) {
+            tc_fence_before();
+            mbar_arrive(bar(C::kBarOFree + i));    // the next unit's products may start
+          }
           if (whole) {
-            if (ROUNDED) {
 #pragma unroll
-              for (int k = 0; k < 64; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * inv);
-              store_rows<8>(stage, lane, nrow, (long long)hr * D + 64 * c, o.f32,
-                             [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
-              store_rows<8>(stage, lane, nrow, (long long)hr * D + 64 * c + 32, o.f32, [&](int k) {
-                return make_uint4(ov[32 + 4 * k], ov[33 + 4 * k], ov[34 + 4 * k], ov[35 + 4 * k]);
-              });
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                ov[k] = Half16<T>::pack(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1]));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                ov[k] = Half16<T>::pack(__uint_as_float(ov[2 * k]) * inv, __uint_as_float(ov[2 * k + 1]) * inv);
-            }
-            store_rows<8>(stage, lane, nrow, at + 64 * c, reinterpret_cast<T *>(o.out),
-                           [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
-          } else if (store) {
-            float4 *ps = reinterpret_cast<float4 *>(slot + 2 * C::kRows);
+            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * inv);
+            if (ROUNDED)
+              store_rows<8>(stage, lane, nrow, (long long)hr * D + 32 * c, o.f32,
+                            [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              ps[(size_t)(16 * c + k) * C::kRows + prow] =
+              ov[k] = Half16<T>::pack(__uint_as_float(ov[2 * k]), __uint_as_float(ov[2 * k + 1]));
+            store_rows<4>(stage, lane, nrow, at + 32 * c, reinterpret_cast<T *>(o.out),
+                          [&](int k) { return make_uint4(ov[4 * k], ov[4 * k + 1], ov[4 * k + 2], ov[4 * k + 3]); });
+          } else if (store) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              ps[(size_t)(8 * c + k) * C::kRows] =
                   make_float4(__uint_as_float(ov[4 * k]), __uint_as_float(ov[4 * k + 1]),
                               __uint_as_float(ov[4 * k + 2]), __uint_as_float(ov[4 * k + 3]));
           }
         }
-        tc_fence_before();
-        mbar_arrive(bar(C::kBarOFree + i));
       }
-      if (!whole && s.ta == 0 && tid == 128) cuts[blockIdx.x] = packed_cut(*start, s);
+      if (!whole && s.ta == 0 && tid == 128) cuts[blockIdx.x] = packed_cut(p, *start, s, gridDim.x);
     }
     if (!ok) *abort = 1;
   }

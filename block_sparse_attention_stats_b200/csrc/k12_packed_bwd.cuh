@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(320, 1)
                       long long out1_head, long long out1_row, PackedCut *__restrict__ cuts,
                       float *__restrict__ part) {
   using C = PackedBwdCfg<D, KV>;
-  using Cost = typename std::conditional<KV, KeyCost, RowCost<kKeyTile>>::type;
+  using Cost = typename std::conditional<KV, KeyCost, RowCost>::type;
   using namespace sm100;
   constexpr int kStages = C::kStages, kMisc = C::kOffMisc;
   extern __shared__ unsigned char smem_raw[];
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(320, 1)
       }
       tc_fence_before();
       mbar_arrive(bar(C::kBarAccFree));
-      if (!whole && s.ta == 0 && tid == 64) cuts[blockIdx.x] = packed_cut(*start, s);
+      if (!whole && s.ta == 0 && tid == 64) cuts[blockIdx.x] = packed_cut(p, *start, s, gridDim.x);
     }
     if (!ok) *abort = 1;
   }
@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(128)
                   (long long)gridDim.x * gridDim.y * blockDim.x);
   const PackedCut cut = packed_cut_at(cuts, blockIdx.x);
   if (!cut.valid) return;
-  const PackedRequest r = packed_request(p, cut.b);
+  bool bad = false;
+  const PackedRequest r = packed_request(p, cut.b, bad);
   const int per = KV ? 128 : p.tq, g = KV ? 1 : p.G, tok0 = cut.rt * per;
   const int rows = min(r.n - tok0, per) * g;
   const int c0 = blockIdx.x, n = cut.last - c0 + 1;

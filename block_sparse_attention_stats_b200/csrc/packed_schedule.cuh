@@ -4,17 +4,22 @@
 // cu[b+1] - 1 of q, and its tokens are the last n of its kv positions (for
 // packed prompts kv = n).  A unit is (sequence, row tile, key head): tq tokens
 // times the G query heads of the key head, G rows a token, against the key
-// tiles of 128 positions that the tile's last token sees.  All units' key
-// tiles, laid end to end, are cut into as many equal ranges as there are CTAs,
-// so every CTA gets the same number of tiles whatever the lengths are.  Nothing
-// is read on the host: the cut depends on lengths in device memory alone, and
-// the grid on the device alone, so a captured launch serves any lengths.
-// A unit counts unit_cost tiles more than it has, for what its start and its end
-// take: without, a CTA that got many short units ran twice as long as the others.
-// A cut that would fall into these is moved to the unit's start.
+// positions that the tile's last token sees, in tiles of 128.  All units, each as
+// long as its positions, are laid end to end, and the line is cut into equal
+// ranges, one a CTA, so every CTA gets the same number of tiles (to within one)
+// whatever the lengths are.  Nothing is read on the host: the cut depends on
+// lengths in device memory alone, and the grid on the device alone, so a captured
+// launch serves any lengths.
+// Lengths in positions, not in tiles, make what lies before a unit a polynomial of
+// its number, so a CTA finds its place with a few multiplications; a cut counts
+// for the tile that it falls into.  (Exact sums of rounded tiles, with 64-bit
+// divisions, took 4 us at the start of every kernel.)
+// A unit counts unit_cost positions more than it has, for what its start and its
+// end take: without, a CTA that got many short units ran twice as long as the
+// others.  A cut that falls into these is one at the unit's start.
 // A unit inside one range is written by its CTA.  A unit cut by a range's end
-// leaves float32 partial sums, and combine_kernel joins them in ascending CTA
-// order (no atomics: the same inputs give the same bits).
+// leaves float32 partial sums, and packed_combine_kernel joins them in ascending
+// CTA order (no atomics: the same inputs give the same bits).
 #pragma once
 
 #include <math.h>
@@ -33,8 +38,8 @@ struct PackedProblem {
   int causal;
   int tq;                   // tokens of a row tile
   int max_kv;               // most key positions a sequence can have (table width x page size)
-  int min_tiles;            // no range is cut shorter than this
-  int unit_cost;            // what a unit takes beside its tiles, in tiles
+  int unit_cost;            // what a unit takes beside its positions, in positions
+  int min_range;            // no range is shorter than this, at least a tile
 };
 
 struct PackedRequest {
@@ -42,122 +47,115 @@ struct PackedRequest {
 };
 
 // Offsets and lengths are device data: whatever they hold, rows stay inside
-// [0, T) and positions inside [0, max_kv].
-__device__ __forceinline__ PackedRequest packed_request(const PackedProblem &p, int b) {
+// [0, T) and positions inside [0, max_kv]; `bad` is set where they did not.
+__device__ __forceinline__ PackedRequest packed_request(const PackedProblem &p, int b, bool &bad) {
   PackedRequest r;
   const int lo = sm100::ld_int(p.cu + b), hi = sm100::ld_int(p.cu + b + 1);
+  const int kv = p.kv_lens ? sm100::ld_int(p.kv_lens + b) : 0;
   r.first = min(max(lo, 0), p.T);
   r.n = max(min(hi, p.T) - r.first, 0);
-  r.kv = r.n;
-  if (p.kv_lens) r.kv = min(max(sm100::ld_int(p.kv_lens + b), 0), p.max_kv);
+  r.kv = p.kv_lens ? min(max(kv, 0), p.max_kv) : r.n;
   r.past = r.kv - r.n;
+  bad = bad || lo < 0 || hi < lo || hi > p.T || kv < 0 || kv > p.max_kv;
   return r;
 }
 
-__device__ __forceinline__ bool packed_request_malformed(const PackedProblem &p, int b) {
-  const int lo = sm100::ld_int(p.cu + b), hi = sm100::ld_int(p.cu + b + 1);
-  bool bad = lo < 0 || hi < lo || hi > p.T;
-  if (p.kv_lens) {
-    const int kv = sm100::ld_int(p.kv_lens + b);
-    bad = bad || kv < 0 || kv > p.max_kv;
-  }
-  return bad;
-}
-
-// sum of floor((a i + b) / m) for i = 0 .. n - 1 (the Euclidean recursion on
-// the lattice points under a line); a, m <= 2^8, b < 2^31, a n < 2^31
-__host__ __device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  long long s = 0;
-  while (n) {
-    s += (long long)(a / m) * ((long long)n * (n - 1) / 2) + (long long)(b / m) * n;
-    a %= m;
-    b %= m;
-    const unsigned y = a * n + b;
-    n = y / m;
-    b = y % m;
-    const unsigned t = m;
-    m = a;
-    a = t;
-    if (m == 0) break;
-  }
-  return s;
-}
-
-// What a unit costs, in tiles.  RowCost<KT>: a unit is a row tile of tq tokens,
-// its tiles are the KT-key tiles that the last token sees (at least one: a row
-// without keys is still written).  KeyCost: a unit is a tile of 128 keys of a
-// sequence over itself, its tiles are the 128-token tiles of every query head
-// that see it.  before(..., rt): the tiles of units 0 .. rt - 1 of a key head.
-template <int KT> struct RowCost {
+// Units of a sequence, the length of one (without unit_cost), the lengths of those
+// before it, and about which one starts y positions on.  RowCost: a unit is a row
+// tile of tq tokens.  KeyCost: a unit is a tile of 128 keys of a sequence over
+// itself, its length the 128-token tiles of every query head that see it.
+struct RowCost {
   static __host__ __device__ int units(const PackedProblem &p, int n) { return n > 0 ? (n - 1) / p.tq + 1 : 0; }
-  static __host__ __device__ int tiles(const PackedProblem &p, int n, int kv, int tq, int rt) {
-    const long long past = kv > n ? kv - n : 0;
-    const long long upto = (long long)(rt + 1) * tq;
-    const long long end = p.causal ? past + (n < upto ? n : upto) : (kv > 1 ? kv : 1);
-    return (int)((end + KT - 1) / KT);
+  // positions that row tile rt of tq tokens sees (at least one: a row without keys is still written)
+  static __host__ __device__ int length(const PackedProblem &p, int n, int kv, int tq, int rt) {
+    const int past = kv > n ? kv - n : 0;
+    return p.causal ? past + (n - rt * tq < tq ? n : (rt + 1) * tq) : (kv > 1 ? kv : 1);
   }
-  static __host__ __device__ int tiles(const PackedProblem &p, int n, int kv, int rt) {
-    return tiles(p, n, kv, p.tq, rt);
+  static __host__ __device__ int length(const PackedProblem &p, int n, int kv, int rt) {
+    return length(p, n, kv, p.tq, rt);
   }
   static __host__ __device__ long long before(const PackedProblem &p, int n, int kv, int rt) {
-    const int R = units(p, n);
-    if (rt <= 0 || R == 0) return 0;
-    if (!p.causal) return (long long)rt * tiles(p, n, kv, 0);
     const int past = kv > n ? kv - n : 0;
-    const int whole = rt < R ? rt : R - 1;   // units of tq tokens
-    long long s = floor_sum((unsigned)whole, KT, (unsigned)p.tq, (unsigned)past + (unsigned)p.tq + KT - 1);
-    if (rt >= R) s += tiles(p, n, kv, R - 1);
-    return s;
+    if (!p.causal) return (long long)rt * (kv > 1 ? kv : 1);
+    return (long long)rt * past + (long long)p.tq * ((long long)rt * (rt + 1) / 2);
+  }
+  static __device__ int guess(const PackedProblem &p, int n, int kv, float y) {
+    if (!p.causal) return (int)(y / (float)((kv > 1 ? kv : 1) + p.unit_cost));
+    const float b = (float)(kv > n ? kv - n : 0) + p.unit_cost + 0.5f * p.tq;
+    return (int)(2.f * y / (b + sqrtf(fmaf(b, b, 2.f * p.tq * y))));
   }
 };
 struct KeyCost {
   static __host__ __device__ int units(const PackedProblem &, int n) { return (n + kKeyTile - 1) / kKeyTile; }
-  static __host__ __device__ int tiles(const PackedProblem &p, int n, int, int rt) {
-    return p.G * (units(p, n) - (p.causal ? rt : 0));
+  static __host__ __device__ int length(const PackedProblem &p, int n, int, int rt) {
+    return kKeyTile * p.G * (units(p, n) - (p.causal ? rt : 0));
   }
   static __host__ __device__ long long before(const PackedProblem &p, int n, int, int rt) {
     const long long N = units(p, n);
-    return p.G * (rt * N - (p.causal ? (long long)rt * (rt - 1) / 2 : 0));
+    return kKeyTile * p.G * (rt * N - (p.causal ? (long long)rt * (rt - 1) / 2 : 0));
+  }
+  static __device__ int guess(const PackedProblem &p, int n, int, float y) {
+    const float g = (float)kKeyTile * p.G, N = (float)units(p, n);
+    if (!p.causal) return (int)(y / (g * N + p.unit_cost));
+    const float b = g * (N + 0.5f) + p.unit_cost;
+    return (int)(2.f * y / (b + sqrtf(fmaxf(fmaf(b, b, -2.f * g * y), 0.f))));
   }
 };
+__host__ __device__ inline int packed_tiles(int length) { return (length + kKeyTile - 1) / kKeyTile; }
 
-// what all key heads' units before row tile rt count
+// what units 0 .. rt - 1 of a sequence count, over all key heads
 template <class Cost>
 __host__ __device__ __forceinline__ long long packed_before(const PackedProblem &p, const PackedRequest &r, int rt) {
   return p.Hkv * (Cost::before(p, r.n, r.kv, rt) + (long long)rt * p.unit_cost);
 }
-
 template <class Cost>
-__device__ __forceinline__ long long packed_cost(const PackedProblem &p, const PackedRequest &r) {
-  return packed_before<Cost>(p, r, Cost::units(p, r.n));
+__host__ __device__ __forceinline__ long long packed_cost(const PackedProblem &p, const PackedRequest &r) {
+  const int R = Cost::units(p, r.n);
+  if (R == 0) return 0;
+  return packed_before<Cost>(p, r, R - 1) + p.Hkv * (long long)(Cost::length(p, r.n, r.kv, R - 1) + p.unit_cost);
 }
 
+// Where a CTA's range starts: `at` positions into unit (b, rt, h), `left` positions long
 struct PackedStart {
-  long long total;    // key tiles of the whole problem
-  long long w0, w1;   // this CTA's range
-  long long rem;      // w0's distance from the first tile of sequence b
-  int b, ctas;        // sequence of w0; CTAs that have a range
+  long long left, end, chunk;   // end: the range's end on the line; chunk: the length of a range
+  int b, rt, h, at;
+  PackedRequest r;
 };
 
-__host__ __device__ __forceinline__ long long packed_range_start(long long total, int ctas, int c) {
-  return total * c / ctas;
+// Row tile, key head and offset of the point `rem` positions into sequence r.
+template <class Cost>
+__device__ __forceinline__ void packed_point(const PackedProblem &p, const PackedRequest &r, long long rem,
+                                             int &rt, int &h, int &at) {
+  const int R = Cost::units(p, r.n);
+  int x = min(max(Cost::guess(p, r.n, r.kv, (float)rem / (float)p.Hkv), 0), R - 1);
+  while (x > 0 && packed_before<Cost>(p, r, x) > rem) --x;
+  while (x + 1 < R && packed_before<Cost>(p, r, x + 1) <= rem) ++x;
+  const long long in = rem - packed_before<Cost>(p, r, x);
+  const int all = Cost::length(p, r.n, r.kv, x) + p.unit_cost;
+  int y = min(max((int)((float)in / (float)all), 0), p.Hkv - 1);
+  while (y > 0 && (long long)y * all > in) --y;
+  while (y + 1 < p.Hkv && (long long)(y + 1) * all <= in) ++y;
+  rt = x;
+  h = y;
+  at = (int)(in - (long long)y * all);
 }
 
 // One call by all `threads` threads of a CTA (a multiple of 32, at most 512):
 // fills *out (shared memory).  Contains two CTA barriers.
 template <class Cost>
-__device__ __forceinline__ void packed_locate(const PackedProblem &p, int cta, int grid, int tid,
-                                              int threads, long long *warp_sum, PackedStart *out) {
+__device__ __forceinline__ void packed_locate(const PackedProblem &p, int cta, int grid, int tid, int threads,
+                                              long long *warp_sum, PackedStart *out) {
   const int per = (p.B + threads - 1) / threads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long own = 0;
   bool bad = false;
+  PackedRequest r{};
   for (int b = b0; b < b1; ++b) {
-    own += packed_cost<Cost>(p, packed_request(p, b));
-    bad = bad || packed_request_malformed(p, b);
+    r = packed_request(p, b, bad);
+    own += packed_cost<Cost>(p, r);
   }
   if (bad && cta == 0) report_device_error(kDevErrRange);
-  const int lane = tid & 31, warp = tid >> 5;
+  const int lane = tid & 31, warp = tid >> 5, warps = threads >> 5;
   long long incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -166,45 +164,47 @@ __device__ __forceinline__ void packed_locate(const PackedProblem &p, int cta, i
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  long long before = incl - own, total = 0;
-  for (int w = 0; w < threads / 32; ++w) {
-    const long long s = warp_sum[w];
-    if (w < warp) before += s;
-    total += s;
+  // sums of the warps before this one, and of all
+  long long sum = lane < warps ? warp_sum[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
   }
-  const long long want = total / p.min_tiles;
-  const int ctas = want < 1 ? 1 : want < grid ? (int)want : grid;
-  const long long w0 = cta < ctas ? packed_range_start(total, ctas, cta) : total;
-  const long long w1 = cta < ctas ? packed_range_start(total, ctas, cta + 1) : total;
-  if (tid == 0 && w0 >= total) {
-    out->total = total;
-    out->w0 = out->w1 = total;
-    out->rem = 0;
-    out->b = p.B;
-    out->ctas = ctas;
-  }
-  if (own > 0 && w0 >= before && w0 < before + own) {
+  const long long total = __shfl_sync(0xffffffffu, sum, warps - 1);
+  const long long up_to = __shfl_sync(0xffffffffu, sum, max(warp - 1, 0));
+  const long long before = (warp ? up_to : 0) + incl - own;
+  long long chunk = (long long)((double)total * (1.0 / grid)) + 1;
+  if (chunk < p.min_range) chunk = p.min_range;
+  const long long w0 = chunk * cta < total ? chunk * cta : total;
+  const long long w1 = cta + 1 < grid && chunk * (cta + 1) < total ? chunk * (cta + 1) : total;
+  if (w0 >= total) {
+    if (tid == 0) out->left = 0;
+  } else if (own > 0 && w0 >= before && w0 < before + own) {
     long long rem = w0 - before;
     int b = b0;
-    for (;; ++b) {
-      const long long c = packed_cost<Cost>(p, packed_request(p, b));
-      if (rem < c) break;
-      rem -= c;
-    }
-    out->total = total;
-    out->w0 = w0;
-    out->w1 = w1;
-    out->rem = rem;
+    if (per > 1)
+      for (;; ++b) {
+        r = packed_request(p, b, bad);
+        const long long c = packed_cost<Cost>(p, r);
+        if (rem < c) break;
+        rem -= c;
+      }
+    packed_point<Cost>(p, r, rem, out->rt, out->h, out->at);
+    out->left = w1 - w0;
+    out->end = w1;
+    out->chunk = chunk;
     out->b = b;
-    out->ctas = ctas;
+    out->r = r;
   }
   __syncthreads();
 }
 
-// The part [ta, tb) of one unit's key tiles [0, nt)
+// The part [ta, tb) of one unit's tiles [0, nt)
 struct PackedSegment {
   PackedRequest r;
   int b, rt, h, nt, ta, tb;
+  int end;   // where the segment ends in its unit, in positions
   __device__ __forceinline__ bool whole() const { return ta == 0 && tb == nt; }
   // partial slot of the CTA: 0 holds a unit begun by an earlier CTA, 1 one that goes on in the next
   __device__ __forceinline__ int slot() const { return ta != 0 ? 0 : 1; }
@@ -214,58 +214,51 @@ struct PackedSegment {
 // hold the same values), so no role waits for another to learn what comes next.
 template <class Cost> struct PackedWalk {
   PackedSegment s;
-  long long left;   // of the range, counted like the units
-  int at;           // where the next segment starts in its unit, counted like the unit
-  static constexpr int kDone = -1;
-  // all 32 lanes of a converged warp
+  long long left;   // positions of the range
+  int at, len;      // where the next segment starts in its unit, and the unit's length
   __device__ __forceinline__ void begin(const PackedProblem &p, const PackedStart &st) {
-    left = st.w1 - st.w0;
-    at = 0;
-    s.b = st.b;
-    s.rt = 0;
-    s.h = 0;
+    left = st.left;
     if (left <= 0) return;
-    s.r = packed_request(p, s.b);
-    // last row tile that starts at or before rem: 32-way search
-    int lo = 0, hi = Cost::units(p, s.r.n);   // answer in [lo, hi)
-    const int lane = threadIdx.x & 31;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, x = lo + lane * step;
-      const bool ok = x < hi && packed_before<Cost>(p, s.r, x) <= st.rem;
-      const unsigned m = __ballot_sync(0xffffffffu, ok);   // lane 0 always holds
-      const int last = 31 - __clz(m);
-      lo += last * step;
-      hi = min(hi, lo + step);
-    }
-    s.rt = lo;
-    s.nt = Cost::tiles(p, s.r.n, s.r.kv, lo);
-    const long long in = st.rem - packed_before<Cost>(p, s.r, lo);
-    s.h = (int)(in / (s.nt + p.unit_cost));
-    at = (int)(in % (s.nt + p.unit_cost));
+    s.b = st.b;
+    s.rt = st.rt;
+    s.h = st.h;
+    s.r = st.r;
+    at = st.at;
+    len = Cost::length(p, s.r.n, s.r.kv, s.rt);
+    s.nt = packed_tiles(len);
+  }
+  // tiles that lie before position x of a unit
+  static __device__ __forceinline__ int tiles_before(const PackedProblem &p, int x) {
+    return x <= p.unit_cost ? 0 : packed_tiles(x - p.unit_cost);
   }
   __device__ __forceinline__ bool next(const PackedProblem &p) {
-    if (left <= 0) return false;
-    if (at == kDone) {
-      at = 0;
-      if (++s.h == p.Hkv) {
-        s.h = 0;
-        if (++s.rt >= Cost::units(p, s.r.n)) {
-          s.rt = 0;
-          do {
-            if (++s.b >= p.B) return false;   // cannot happen while tiles are left
-            s.r = packed_request(p, s.b);
-          } while (s.r.n == 0);
+    while (left > 0) {
+      const int all = len + p.unit_cost;
+      if (at == all) {   // the next unit
+        at = 0;
+        if (++s.h == p.Hkv) {
+          s.h = 0;
+          if (++s.rt >= Cost::units(p, s.r.n)) {
+            s.rt = 0;
+            bool bad;
+            do {
+              if (++s.b >= p.B) return false;   // cannot happen while positions are left
+              s.r = packed_request(p, s.b, bad);
+            } while (s.r.n == 0);
+          }
+          len = Cost::length(p, s.r.n, s.r.kv, s.rt);
+          s.nt = packed_tiles(len);
         }
-        s.nt = Cost::tiles(p, s.r.n, s.r.kv, s.rt);
+        continue;
       }
+      s.end = (int)(left < all - at ? at + left : all);
+      s.ta = tiles_before(p, at);
+      s.tb = tiles_before(p, s.end);
+      left -= s.end - at;
+      at = s.end;
+      if (s.tb > s.ta) return true;   // else both ends fall into one tile, or before the first
     }
-    const int all = s.nt + p.unit_cost;
-    const int end = (int)(left < all - at ? at + left : all);
-    left -= end - at;
-    s.ta = max(at - p.unit_cost, 0);
-    s.tb = max(end - p.unit_cost, 0);
-    at = end == all ? kDone : end;
-    return s.tb > s.ta;   // else the range ends before the unit's first tile: the next CTA has it all
+    return false;
   }
 };
 
@@ -279,14 +272,17 @@ __device__ __forceinline__ PackedCut packed_cut_at(const PackedCut *cuts, int c)
   return PackedCut{__ldcg(x), __ldcg(x + 1), __ldcg(x + 2), __ldcg(x + 3), __ldcg(x + 4)};
 }
 
-__device__ __forceinline__ PackedCut packed_cut(const PackedStart &st, const PackedSegment &s) {
+// (a range is at least a tile long, so every CTA between the first and the last has a part)
+__device__ __forceinline__ PackedCut packed_cut(const PackedProblem &p, const PackedStart &st,
+                                                const PackedSegment &s, int grid) {
   PackedCut c;
   c.valid = 1;
   c.b = s.b;
   c.rt = s.rt;
   c.h = s.h;
-  const long long end = st.w1 + (s.nt - s.tb) - 1;   // the unit's last tile
-  c.last = (int)(((end + 1) * st.ctas - 1) / st.total);
+  const long long start = st.end - s.end;   // the unit's, on the line
+  const long long tile = (start + p.unit_cost + (long long)(s.nt - 1) * kKeyTile) / st.chunk;
+  c.last = tile < grid ? (int)tile : grid - 1;
   return c;
 }
 
@@ -328,12 +324,15 @@ __device__ __forceinline__ void store_rows(unsigned char *stage, int lane, int r
 #pragma unroll
   for (int k = 0; k < CH; ++k) *reinterpret_cast<uint4 *>(stage + 16 * slot(lane, k)) = chunk(k);
   __syncwarp();
+  uint4 v[CH];
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+    v[k] = *reinterpret_cast<const uint4 *>(stage + 16 * slot(k * (32 / CH) + lane / CH, lane % CH));
 #pragma unroll
   for (int k = 0; k < CH; ++k) {
-    const int r = k * (32 / CH) + lane / CH, c = lane % CH;
+    const int r = k * (32 / CH) + lane / CH;
     const long long a = __shfl_sync(0xffffffffu, at, r);
-    const uint4 v = *reinterpret_cast<const uint4 *>(stage + 16 * slot(r, c));
-    if (r < rows) *reinterpret_cast<uint4 *>(dst + a + c * (16 / (int)sizeof(E))) = v;
+    if (r < rows) *reinterpret_cast<uint4 *>(dst + a + (lane % CH) * (16 / (int)sizeof(E))) = v[k];
   }
 }
 
@@ -374,7 +373,8 @@ __global__ void __launch_bounds__(128)
                   (long long)gridDim.x * gridDim.y * blockDim.x);
   const PackedCut cut = packed_cut_at(cuts, blockIdx.x);
   if (!cut.valid) return;
-  const PackedRequest r = packed_request(p, cut.b);
+  bool bad = false;
+  const PackedRequest r = packed_request(p, cut.b, bad);
   const int tok0 = cut.rt * p.tq, rows = min(r.n - tok0, p.tq) * p.G;
   const size_t slot = packed_slot_floats<D>(R);
   const int c0 = blockIdx.x, n = cut.last - c0 + 1;

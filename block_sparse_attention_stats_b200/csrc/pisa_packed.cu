@@ -47,10 +47,10 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
   using C = AttendCfg<D>;
   const int tq1 = 128 / p.G;
   p.tq = 2 * tq1;
-  // a unit's start and end take about two tiles, four with the float32 output (measured: 2 / 3 / 4 give
-  // 872 / 876 / 881 us on 12000 + 700 + 4608 tokens, and 2521 / 2430 us a training step at 2 / 3)
-  p.unit_cost = ROUNDED ? 4 : 2;
-  p.min_tiles = p.unit_cost + 1;
+  // a unit's start and end take about three tiles, four with the float32 output (measured at 2 / 2.5 / 3 /
+  // 3.5: 964 / 899 / 882 / 876 us on 12000 + 700 + 4608 tokens, 126 / 128 / 127 / 132 us on 16 x 1000)
+  p.unit_cost = (ROUNDED ? 4 : 3) * kKeyTile;
+  p.min_range = p.unit_cost + kKeyTile;
   CUtensorMap mq;
   PISA_TRY(map_query(&mq, q, Half16<T>::kBf16, D, p.G, p.T, p.Hkv, tq1));
   const PackedScratch s = packed_scratch(D, C::kRows);
@@ -69,8 +69,8 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
                                cudaStream_t st) {
   using C = RowsCfg<D, R>;
   p.tq = R / p.G;
-  p.min_tiles = 1;
-  p.unit_cost = 1;
+  p.unit_cost = 3 * kKeyTile / 2;
+  p.min_range = kKeyTile;
   const PackedScratch s = packed_scratch(D, R);
   PackedCut *cuts = (PackedCut *)(ws + s.cuts);
   float *part = (float *)(ws + s.part);
@@ -131,7 +131,7 @@ static PackedProblem problem(const int32_t *cu, const int32_t *kv_lens, int B, i
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
   p.causal = causal != 0;
-  p.max_kv = (int)std::min<long long>(max_kv, 0x7fffff00ll);
+  p.max_kv = (int)std::min<long long>(max_kv, 1 << 30);
   return p;
 }
 

@@ -47,8 +47,8 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
       (const __nv_bfloat16 *)dout.data, dout.head_stride, dout.row_stride, out_f32, lse, p.Hq, p.T, p.cu, p.B,
       lse2, delta));
   p.tq = 128 / p.G;
-  p.min_tiles = 4;
-  p.unit_cost = 2;
+  p.unit_cost = 5 * kKeyTile / 2;
+  p.min_range = 4 * kKeyTile;
   CUtensorMap mq, mdo, mk, mv;
   PISA_TRY(map_query(&mq, q, true, D, p.G, p.T, p.Hkv, p.tq));
   PISA_TRY(map_query(&mdo, dout, true, D, p.G, p.T, p.Hkv, p.tq));
@@ -94,6 +94,8 @@ pisa_status pisa_varlen_attention_bwd(pisa_rows q, pisa_rows k, pisa_rows v, pis
   if (dtype != PISA_BF16 && dtype != PISA_F16 && dtype != PISA_F32) return PISA_ERR_INVALID_ARG;
   if (dtype != PISA_BF16 || (d != 64 && d != 128)) return PISA_ERR_UNSUPPORTED;
   if (Hq > 65535 || Hq / Hkv > 128 || T > (1 << 24) || B > (1 << 24)) return PISA_ERR_UNSUPPORTED;
+  // a key tile's length, the 128-row tiles of its whole group, is counted in 32 bits
+  if ((long long)ceil_div(T, 128) * 128 * (Hq / Hkv) > (1 << 30)) return PISA_ERR_UNSUPPORTED;
   if (!(scale >= 0.f) || !std::isfinite(scale) || (flags & ~(PISA_CAUSAL | PISA_ZERO_TAIL))) return PISA_ERR_INVALID_ARG;
   if (!cu_seqlens || ((uintptr_t)cu_seqlens & 3u)) return PISA_ERR_INVALID_ARG;
   if (T == 0) return PISA_OK;
