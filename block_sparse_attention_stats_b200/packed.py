@@ -20,37 +20,29 @@ from .api import _check, _require
 _DT = {torch.bfloat16: L.PISA_BF16, torch.float16: L.PISA_F16}
 
 
-def _stream_of(t, stream):
-    """(stream handle, context or None): the context makes the tensor's device and `stream`
-    current, so that memory allocated for the call belongs to the stream that uses it."""
+def _elsewhere(t, stream):
+    """A context that makes the tensor's device and `stream` current, so that memory allocated for
+    the call belongs to the stream that uses it; None where they are already."""
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    if stream is None and torch.cuda.current_device() == t.get_device():
-        return _raw_stream(t.get_device()), None
-    dev = t.device
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
-    with torch.cuda.device(dev):
-        stream = stream or torch.cuda.current_stream(dev)
+    if stream is None:
+        if _current_device() == t.get_device():
+            return None
+        with torch.cuda.device(t.device):
+            stream = torch.cuda.current_stream()
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {t.device}")
     # entering a stream's context makes its device current too
-    return stream.cuda_stream, torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
-def _call_on(t, stream, body):
-    """body(stream handle) with the tensor's device and the stream current."""
-    handle, context = _stream_of(t, stream)
-    if context is None:
-        return body(handle)
-    with context:
-        return body(handle)
-
-
-def _raw_stream(index) -> int:
+def _current_stream(index) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# the handle without the stream object around it, where this torch has that
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+# the current device, and the stream's handle without an object around it, where this torch has them
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
 def _strides_ok(t) -> bool:
@@ -99,7 +91,8 @@ def _dense(t, shape, dtype, name, like) -> Optional[int]:
     """Pointer of a dense array of that shape on like's device (None for None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != like.get_device() or not t.is_contiguous():
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != like.get_device()):
         if t.device != like.device:
             raise ValueError(f"{name} must live on {like.device}")
         _require(t, shape, dtype, name)
@@ -125,9 +118,17 @@ def _heads(q, k, v):
     return hq, T, d, hkv
 
 
-def _scratch(workspace, need, like):
-    """(tensor, pointer, bytes) of the call's scratch memory."""
+_sizes = {}
+
+
+def _scratch(workspace, size, like, *args):
+    """(tensor, pointer, bytes) of the call's scratch memory; size(*args) bytes are needed."""
     if workspace is None:
+        need = _sizes.get((size, args))
+        if need is None:
+            if len(_sizes) > 1000:
+                _sizes.clear()
+            need = _sizes[size, args] = getattr(L.load(), size)(*args)
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
         return workspace, workspace.data_ptr(), need
     if workspace.device != like.device or not workspace.is_contiguous():
@@ -146,27 +147,27 @@ def pisa_varlen_attention(q, k, v, cu_seqlens, causal: bool = True, scale: Optio
     [Hkv, T, d] (bf16 or float16), cu_seqlens int32 [B + 1] on the device.  `lse` (float32
     [Hq, T]) and `out_f32` (float32 [Hq, T, d]) are written if given; the backward needs both.
     Rows of `out` behind the last sequence keep what they held, or become zero with `zero_tail`."""
-    lib = L.load()
     Hq, T, d, Hkv = _heads(q, k, v)
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return pisa_varlen_attention(q, k, v, cu_seqlens, causal, scale, out, lse, out_f32, workspace,
+                                         zero_tail=zero_tail)
     B = cu_seqlens.numel() - 1
-    flags = (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0)
-
-    def body(st):
-        o = torch.empty_like(q) if out is None else out
-        if o.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-        ws, ptr, size = _scratch(workspace, lib.pisa_varlen_attention_workspace_bytes(Hq, Hkv, d), q)
-        status = lib.pisa_varlen_attention(
-            _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"), _DT[q.dtype],
-            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), B, T, Hq, Hkv, d,
-            0.0 if scale is None else float(scale), flags, _rows(o, q, "out"),
-            _dense(lse, (Hq, T), torch.float32, "lse", q),
-            _dense(out_f32, (Hq, T, d), torch.float32, "out_f32", q), ptr, size, st)
-        if status:
-            _check("pisa_varlen_attention", status)
-        return o
-
-    return _call_on(q, stream, body)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    ws, ptr, size = _scratch(workspace, "pisa_varlen_attention_workspace_bytes", q, Hq, Hkv, d)
+    status = L.load().pisa_varlen_attention(
+        _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"), _DT[q.dtype],
+        _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), B, T, Hq, Hkv, d, 0.0 if scale is None else float(scale),
+        (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0), _rows(out, q, "out"),
+        _dense(lse, (Hq, T), torch.float32, "lse", q),
+        _dense(out_f32, (Hq, T, d), torch.float32, "out_f32", q), ptr, size, _current_stream(q.get_device()))
+    if status:
+        _check("pisa_varlen_attention", status)
+    return out
 
 
 def pisa_varlen_attention_bwd(q, k, v, dout, lse, out_f32, cu_seqlens, causal: bool = True,
@@ -176,33 +177,31 @@ def pisa_varlen_attention_bwd(q, k, v, dout, lse, out_f32, cu_seqlens, causal: b
                               zero_tail: bool = False):
     """Gradients (dq, dk, dv) of pisa_varlen_attention (bf16), from the lse and out_f32 of one
     forward call that was given both."""
-    lib = L.load()
     Hq, T, d, Hkv = _heads(q, k, v)
     if dout.shape != q.shape:
         raise ValueError("dout must have the shape of q")
     if lse is None or out_f32 is None:
         raise ValueError("the backward takes the forward's lse and out_f32")
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return pisa_varlen_attention_bwd(q, k, v, dout, lse, out_f32, cu_seqlens, causal, scale, grads,
+                                             workspace, zero_tail=zero_tail)
     B = cu_seqlens.numel() - 1
-    flags = (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0)
-
-    def body(st):
-        dq, dk, dv = grads if grads is not None else (torch.empty_like(q), torch.empty_like(k),
-                                                      torch.empty_like(v))
-        if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
-            raise ValueError("grads must have the shapes of q, k, v")
-        ws, ptr, size = _scratch(workspace, lib.pisa_varlen_attention_bwd_workspace_bytes(T, Hq, Hkv, d), q)
-        status = lib.pisa_varlen_attention_bwd(
-            _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"), _rows(dout, q, "dout"),
-            _DT[q.dtype], _dense(lse, (Hq, T), torch.float32, "lse", q),
-            _dense(out_f32, (Hq, T, d), torch.float32, "out_f32", q),
-            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), B, T, Hq, Hkv, d,
-            0.0 if scale is None else float(scale), flags, _rows(dq, q, "dq"), _rows(dk, q, "dk"),
-            _rows(dv, q, "dv"), ptr, size, st)
-        if status:
-            _check("pisa_varlen_attention_bwd", status)
-        return dq, dk, dv
-
-    return _call_on(q, stream, body)
+    dq, dk, dv = grads if grads is not None else (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+    if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
+        raise ValueError("grads must have the shapes of q, k, v")
+    ws, ptr, size = _scratch(workspace, "pisa_varlen_attention_bwd_workspace_bytes", q, T, Hq, Hkv, d)
+    status = L.load().pisa_varlen_attention_bwd(
+        _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"), _rows(dout, q, "dout"), _DT[q.dtype],
+        _dense(lse, (Hq, T), torch.float32, "lse", q),
+        _dense(out_f32, (Hq, T, d), torch.float32, "out_f32", q),
+        _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), B, T, Hq, Hkv, d, 0.0 if scale is None else float(scale),
+        (L.PISA_CAUSAL if causal else 0) | (L.PISA_ZERO_TAIL if zero_tail else 0), _rows(dq, q, "dq"),
+        _rows(dk, q, "dk"), _rows(dv, q, "dv"), ptr, size, _current_stream(q.get_device()))
+    if status:
+        _check("pisa_varlen_attention_bwd", status)
+    return dq, dk, dv
 
 
 class _VarlenAttention(torch.autograd.Function):
@@ -262,29 +261,29 @@ def pisa_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens,
     """Attention of the newest tokens of every request, q [Hq, T, d], over its pages: the tokens
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 are the last of request b's kv_lens[b] positions.
     block_table int32 [B, width], cu_seqlens int32 [B + 1], kv_lens int32 [B]."""
-    lib = L.load()
     pages, Hkv, ps, d = _caches(k_cache, v_cache, q)
     if q.dim() != 3 or q.shape[2] != d or block_table.dim() != 2:
         raise ValueError("q must be [Hq, T, d] with the caches' d, block_table [B, width]")
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return pisa_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, scale, out, lse,
+                                        workspace)
     Hq, T, _ = q.shape
     B, width = block_table.shape
-
-    def body(st):
-        o = torch.empty_like(q) if out is None else out
-        if o.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-        ws, ptr, size = _scratch(workspace, lib.pisa_paged_attention_workspace_bytes(Hq, Hkv, d), q)
-        status = lib.pisa_paged_attention(
-            _rows(q, q, "q"), _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"),
-            _DT[q.dtype], pages, ps, _ints(block_table, (B, width), "block_table", q), width,
-            _ints(cu_seqlens, (B + 1,), "cu_seqlens", q), _ints(kv_lens, (B,), "kv_lens", q),
-            B, T, Hq, Hkv, d, 0.0 if scale is None else float(scale), _rows(o, q, "out"),
-            _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size, st)
-        if status:
-            _check("pisa_paged_attention", status)
-        return o
-
-    return _call_on(q, stream, body)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    ws, ptr, size = _scratch(workspace, "pisa_paged_attention_workspace_bytes", q, Hq, Hkv, d)
+    status = L.load().pisa_paged_attention(
+        _rows(q, q, "q"), _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"), _DT[q.dtype], pages, ps,
+        _ints(block_table, (B, width), "block_table", q), width, _ints(cu_seqlens, (B + 1,), "cu_seqlens", q),
+        _ints(kv_lens, (B,), "kv_lens", q), B, T, Hq, Hkv, d, 0.0 if scale is None else float(scale), _rows(out, q, "out"),
+        _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size, _current_stream(q.get_device()))
+    if status:
+        _check("pisa_paged_attention", status)
+    return out
 
 
 def _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out):
@@ -295,8 +294,8 @@ def _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size
     if out is None:
         # the small results share one allocation
         small = torch.empty(2 * B + 2, dtype=torch.int32, device=dev)
-        out = dict(slots=torch.empty(T, dtype=torch.int64, device=dev), cu_seqlens=small[:B + 1],
-                   kv_lens=small[B + 1:-1], num_free=small[-1:])
+        cu, kv, left = small.split((B + 1, B, 1))
+        out = dict(slots=torch.empty(T, dtype=torch.int64, device=dev), cu_seqlens=cu, kv_lens=kv, num_free=left)
     like = block_table
     slots = out["slots"]
     step = L.PisaPageStep(
@@ -314,34 +313,33 @@ def pisa_page_plan(past_lens, new_lens, block_table, free_pages, num_free, page_
     """One step's bookkeeping: enters new pages into block_table [B, width] and returns
     dict(slots int64 [T], cu_seqlens [B + 1], kv_lens [B], num_free [1]).  Pages come from the end
     of free_pages[: num_free]; `out` may pass preallocated results.  All lengths int32."""
-    lib = L.load()
-
-    def body(st):
-        step, res = _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out)
-        status = lib.pisa_page_plan(ctypes.byref(step), st)
-        if status:
-            _check("pisa_page_plan", status)
-        return res
-
-    return _call_on(block_table, stream, body)
+    away = _elsewhere(block_table, stream)
+    if away is not None:
+        with away:
+            return pisa_page_plan(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out)
+    step, out = _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out)
+    status = L.load().pisa_page_plan(ctypes.byref(step), _current_stream(block_table.get_device()))
+    if status:
+        _check("pisa_page_plan", status)
+    return out
 
 
 def pisa_page_write(k, v, slots, k_cache, v_cache, stream=None) -> None:
     """Rows t of k and v [Hkv, T, d] to slot slots[t] (int64; negative: left out) of the caches."""
-    lib = L.load()
     pages, Hkv, ps, d = _caches(k_cache, v_cache, k)
-    if k.dim() != 3 or k.shape != v.shape or k.shape[0] != Hkv or k.shape[2] != d:
+    shape = k.shape
+    if len(shape) != 3 or shape != v.shape or shape[0] != Hkv or shape[2] != d:
         raise ValueError("k and v must be [Hkv, T, d] with the caches' Hkv and d")
-    T = k.shape[1]
-
-    def body(st):
-        status = lib.pisa_page_write(
-            _rows(k, k, "k"), _rows(v, k, "v"), _DT[k.dtype], _dense(slots, (T,), torch.int64, "slots", k),
-            T, Hkv, d, _pages(k_cache, k, "k_cache"), _pages(v_cache, k, "v_cache"), pages, ps, st)
-        if status:
-            _check("pisa_page_write", status)
-
-    _call_on(k, stream, body)
+    away = _elsewhere(k, stream)
+    if away is not None:
+        with away:
+            return pisa_page_write(k, v, slots, k_cache, v_cache)
+    T = shape[1]
+    status = L.load().pisa_page_write(
+        _rows(k, k, "k"), _rows(v, k, "v"), _DT[k.dtype], _dense(slots, (T,), torch.int64, "slots", k), T, Hkv, d,
+        _pages(k_cache, k, "k_cache"), _pages(v_cache, k, "v_cache"), pages, ps, _current_stream(k.get_device()))
+    if status:
+        _check("pisa_page_write", status)
 
 
 def pisa_paged_step(q, k, v, k_cache, v_cache, past_lens, new_lens, block_table, free_pages, num_free,
@@ -350,27 +348,28 @@ def pisa_paged_step(q, k, v, k_cache, v_cache, past_lens, new_lens, block_table,
                     workspace: Optional[torch.Tensor] = None, stream=None):
     """The whole step of a server: plan, write of k and v, attention of q over the pages.
     Returns (out, plan), plan as from pisa_page_plan; `plan` may pass preallocated results."""
-    lib = L.load()
     pages, Hkv, ps, d = _caches(k_cache, v_cache, q)
     Hq, T, dq, hk = _heads(q, k, v)
     if dq != d or hk != Hkv:
         raise ValueError("q, k, v must have the caches' Hkv and d")
     if block_table.device != q.device:
         raise ValueError(f"block_table must live on {q.device}")
-
-    def body(st):
-        o = torch.empty_like(q) if out is None else out
-        if o.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-        step, res = _page_step(past_lens, new_lens, block_table, free_pages, num_free, ps, T, plan)
-        ws, ptr, size = _scratch(workspace, lib.pisa_paged_attention_workspace_bytes(Hq, Hkv, d), q)
-        status = lib.pisa_paged_step(
-            ctypes.byref(step), _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"),
-            _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"), _DT[q.dtype], pages, Hq, Hkv,
-            d, 0.0 if scale is None else float(scale), _rows(o, q, "out"),
-            _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size, st)
-        if status:
-            _check("pisa_paged_step", status)
-        return o, res
-
-    return _call_on(q, stream, body)
+    away = _elsewhere(q, stream)
+    if away is not None:
+        with away:
+            return pisa_paged_step(q, k, v, k_cache, v_cache, past_lens, new_lens, block_table, free_pages,
+                                   num_free, scale, out, plan, lse, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    step, plan = _page_step(past_lens, new_lens, block_table, free_pages, num_free, ps, T, plan)
+    ws, ptr, size = _scratch(workspace, "pisa_paged_attention_workspace_bytes", q, Hq, Hkv, d)
+    status = L.load().pisa_paged_step(
+        ctypes.byref(step), _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"),
+        _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"), _DT[q.dtype], pages, Hq, Hkv, d,
+        0.0 if scale is None else float(scale), _rows(out, q, "out"), _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size,
+        _current_stream(q.get_device()))
+    if status:
+        _check("pisa_paged_step", status)
+    return out, plan
