@@ -10,24 +10,26 @@
 //
 // Work unit (packed_schedule.cuh): two subtiles of 128 rows, each 128 / G tokens
 // with the G query heads of one key head (token-major), so K and V are read once
-// for a group.  Keys come in tiles of 128.
-// Roles (384 threads, one CTA per SM, persistent over its range of tiles):
+// for a group.  Keys come in tiles of 128 and are worked on in halves of 64.
+// Roles (352 threads, one CTA per SM, persistent over its range of tiles):
 //   warp 0      copies: Q of both subtiles, then K and V tiles into a ring;
-//   warp 1      TMEM; issues S_i = Q_i K^T and O_i += P_i V (P read from TMEM);
-//               subtile 0's products run while subtile 1's softmax does, and back;
-//   warps 4-7   softmax of subtile 0, one thread a row (TMEM lane);
-//   warps 8-11  softmax of subtile 1.
-// A softmax thread holds 128 scores: its warpgroups take 200 registers a thread,
-// the first (whose warps 2 and 3 have nothing to do) keeps 104: with the launch's
-// 168 for all, the scores spilled.
-// TMEM columns: S_0 [0, 128), S_1 [128, 256), O_0 [256, 256 + D), O_1 after it;
-// P (16-bit) overwrites the first 64 columns of its S.  S_i of the next tile is
-// issued after P_i V of this one by the same thread, and one thread's products
-// run in issue order, so no barrier guards the overwrite; the commit that tells
-// the softmax of S_i also says that O_i is complete up to the tile before, so a
-// softmax thread may rescale O_i itself.  That is rare: the running maximum moves
-// only when it grows by more than 2^8 (weights stay below 2^8, in range of both
-// 16-bit types).
+//   warps 1, 10 (1: TMEM) issue S_ih = Q_i K_h^T and O_i += P_ih V_h (P read from TMEM)
+//               for subtile 0 and 1 and half h of a tile;
+//   warps 2-5   softmax of subtile 0, one thread a row (TMEM lane);
+//   warps 6-9   softmax of subtile 1.
+// TMEM columns: S_ih [128 i + 64 h, + 64), O_0 [256, 256 + D), O_1 after it; P
+// (16-bit) overwrites the first 32 columns of its S.  While the softmax works on
+// one half, the products of the other run: P V, then S of the next tile's same
+// half.  With whole tiles a subtile's softmax waited 1200 of 3200 cycles for its
+// own P V and S; with halves and one issuing warp, that warp waited for one
+// subtile's weights while the other's were ready.  Measured, whole tiles / halves /
+// halves and two issuing warps: 880 / 952 / 853 us on 12000 + 700 + 4608 tokens (24 /
+// 8 heads, causal), 125 / 110 / 100 us on 16 x 1000 (16 / 16 heads).
+// S_ih of the next tile is issued after P_ih V_h of this one by the same thread, and one
+// thread's products run in order, so no barrier guards the overwrite.
+// The running maximum moves only when it grows by more than 2^8 (weights stay
+// below 2^8, in range of both 16-bit types); a softmax thread then waits for the
+// product before, and rescales O_i itself.
 // Every wait is bounded; on a timeout the CTA records the error, stops issuing,
 // drains its copies and products, frees TMEM and exits.
 #pragma once
@@ -39,9 +41,7 @@
 namespace pisa {
 
 template <int D> struct AttendCfg {
-  static constexpr int kThreads = 384;
-  static constexpr int kRegsSoftmax = 200, kRegsOther = 104;   // of 168 at launch
-  static_assert(2 * kRegsSoftmax + kRegsOther == 3 * 168, "registers");
+  static constexpr int kThreads = 352;
   static constexpr int kRows = 256;                      // rows of a unit
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kTileBytes = kKeyTile * D * 2;    // K or V tile, or Q of a subtile
@@ -52,58 +52,53 @@ template <int D> struct AttendCfg {
   static constexpr int kOffMisc = kOffStage + 8 * 4096;
   static constexpr int kSmem = kOffMisc + 1024 + 1024;   // + alignment slack
   static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarFull = 2, kBarEmpty = kBarFull + kStages;
-  static constexpr int kBarS = kBarEmpty + kStages;      // + subtile
-  static constexpr int kBarP = kBarS + 2;                // P's first 64 columns; + 2: the rest
-  static constexpr int kBarO = kBarP + 4;                // O complete
-  static constexpr int kBarOFree = kBarO + 2;            // O read
+  static constexpr int kBarS = kBarEmpty + kStages;      // + 2 half + subtile
+  static constexpr int kBarP = kBarS + 4;                // + 2 half + subtile
+  static constexpr int kBarPV = kBarP + 4;               // + subtile: a half's product is in O
+  static constexpr int kBarO = kBarPV + 2;               // + subtile: O complete
+  static constexpr int kBarOFree = kBarO + 2;            // + subtile: O read
   static constexpr int kBarTeardown = kBarOFree + 2;
   static_assert(kBarTeardown < 48 && kSmem <= 227 * 1024, "shared memory");
   static constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 };
 
-// tq1 tokens of a subtile; rows of subtile i, and its key tiles
+// tq1 tokens of a subtile; rows of subtile i, and its halves of key tiles
 struct SubTile {
-  int rows, nt;
+  int rows, nh;
 };
 __device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedSegment &s, int tq1, int i) {
   SubTile x;
   const int tok = s.rt * p.tq + i * tq1;
   x.rows = max(min(s.r.n - tok, tq1), 0) * p.G;
-  x.nt = x.rows == 0 ? 0 : packed_tiles(RowCost::length(p, s.r.n, s.r.kv, tq1, 2 * s.rt + i));
+  x.nh = x.rows == 0 ? 0 : (RowCost::length(p, s.r.n, s.r.kv, tq1, 2 * s.rt + i) + 63) / 64;
   return x;
 }
 
-// One row's part of a 128 x 128 tile: scores from TMEM, running maximum and sum,
-// weights back as 16 bits over the scores' first 64 columns, O rescaled where
-// the maximum has moved.  `seen` columns are visible.
+// One row's part of 64 keys: scores from TMEM, running maximum and sum, weights
+// back as 16 bits over the scores' first 32 columns, O rescaled where the maximum
+// has moved (once `pv_done` says that the product before is in it).  `seen` columns
+// are visible.
 // A quarter of the exponentials as a polynomial on the multiply-add units did not
-// pay: 918 against 893 us on 12000 + 700 + 4608 causal tokens, level on 2 x 4096
-// uncut ones (the products and their shared-memory reads bound the tile).
-// ROUNDED (where the float32 output is wanted too): for the backward the sum takes the rounded weights: dout_t . o_t
-// is then the mean of dP under the weights themselves, and does not lose dP -
-// Delta to their rounding where one key holds nearly all the weight.  Otherwise
-// the sum keeps the float32 weights.
-template <typename T, int D, bool ROUNDED>
-__device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, float sl2, int seen,
-                                             uint32_t bar_p, float &m_run, float &l_run) {
+// pay (918 against 893 us on 12000 + 700 + 4608 causal tokens).
+// ROUNDED (where the float32 output is wanted too): for the backward the sum takes
+// the rounded weights: dout_t . o_t is then the mean of dP under the weights
+// themselves, and does not lose dP - Delta to their rounding where one key holds
+// nearly all the weight.  Otherwise the sum keeps the float32 weights.
+template <typename T, int D, bool ROUNDED, typename Wait>
+__device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, float sl2, int seen, Wait pv_done,
+                                             float &m_run, float &l_run) {
   using namespace sm100;
-  uint32_t r[128];
+  uint32_t r[64];
   tmem_ld_x32(s_addr, reinterpret_cast<uint32_t(&)[32]>(r[0]));
   tmem_ld_x32(s_addr + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
   tmem_wait_ld();
-  tmem_ld_x32(s_addr + 64, reinterpret_cast<uint32_t(&)[32]>(r[64]));
-  tmem_ld_x32(s_addr + 96, reinterpret_cast<uint32_t(&)[32]>(r[96]));
   auto sv = [&](int c) -> float { return __uint_as_float(r[c]); };
-  // bit c of word w: column 32 w + c is visible
-  const bool masked = __any_sync(0xffffffffu, seen < kKeyTile);
-  auto word = [&](int w) -> uint32_t {
-    const int n = seen - 32 * w;
-    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-  };
-  if (masked) {
+  if (__any_sync(0xffffffffu, seen < 64)) {
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const uint32_t m = word(w);
+      // bit c: column 32 w + c is visible
+      const int n = seen - 32 * w;
+      const uint32_t m = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
 #pragma unroll
       for (int c = 0; c < 32; ++c) r[32 * w + c] = (m >> c) & 1u ? r[32 * w + c] : 0xff800000u;
     }
@@ -117,65 +112,46 @@ __device__ __forceinline__ void softmax_tile(uint32_t s_addr, uint32_t o_addr, f
     for (int c = 0; c < 8; ++c) mx[c] = max3f(mx[c], sv(c + k), sv(c + k + 8));
 #pragma unroll
   for (int c = 0; c < 8; ++c) mx[c] = fmaxf(mx[c], sv(c + 56));
-  tmem_wait_ld();
-  if (masked) {
-#pragma unroll
-    for (int w = 2; w < 4; ++w) {
-      const uint32_t m = word(w);
-#pragma unroll
-      for (int c = 0; c < 32; ++c) r[32 * w + c] = (m >> c) & 1u ? r[32 * w + c] : 0xff800000u;
-    }
-  }
-#pragma unroll
-  for (int k = 64; k < 128; k += 16)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) mx[c] = max3f(mx[c], sv(c + k), sv(c + k + 8));
   const float tmax = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
   const float m_t = tmax * sl2;
   const bool grow = m_t > m_run + 8.0f;
   const bool need_o = grow && m_run != -INFINITY;
   if (__any_sync(0xffffffffu, need_o)) {
-    const float f = grow ? ex2_approx(m_run - m_t) : 1.0f;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      uint32_t ov[16];
-      tmem_ld_x16(o_addr + 16 * c, ov);
+    if (!pv_done()) return false;
+    tc_fence_after();
+    const float f = need_o ? ex2_approx(m_run - m_t) : 1.0f;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t ov[32];
+      tmem_ld_x32(o_addr + 32 * c, ov);
       tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-      tmem_st_x16(o_addr + 16 * c, ov);
+      for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+      tmem_st_x32(o_addr + 32 * c, ov);
     }
-    l_run *= need_o ? f : 1.f;
+    l_run *= f;
   }
   if (grow) m_run = m_t;
   const float neg = m_run == -INFINITY ? 0.f : -m_run;   // no key seen yet: every weight is zero
   const float2 sl2x2 = make_float2(sl2, sl2), neg2 = make_float2(neg, neg);
   float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t pk[32];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int c = 64 * h + 32 * q + 2 * k;
-        const float2 z = fma2(make_float2(sv(c), sv(c + 1)), sl2x2, neg2);
-        const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
-        pk[k] = Half16<T>::pack(e.x, e.y);
-        acc[k & 1] = add2(acc[k & 1], ROUNDED ? Half16<T>::unpack(pk[k]) : e);
-      }
-      tmem_st_x16(s_addr + 32 * h + 16 * q, pk);
-    }
-    tmem_wait_st();
-    tc_fence_before();
-    mbar_arrive(bar_p + 16 * h);
+  for (int k = 0; k < 32; ++k) {
+    const float2 z = fma2(make_float2(sv(2 * k), sv(2 * k + 1)), sl2x2, neg2);
+    const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+    pk[k] = Half16<T>::pack(e.x, e.y);
+    acc[k & 1] = add2(acc[k & 1], ROUNDED ? Half16<T>::unpack(pk[k]) : e);
   }
+  tmem_st_x32(s_addr, pk);
   const float2 a2 = add2(acc[0], acc[1]);
   l_run += a2.x + a2.y;
+  tmem_wait_st();
+  return true;
 }
 
 template <typename T, int D, bool PAGED, bool ROUNDED>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(352, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PackedProblem p,
                      const PagedKV cache, float scale, const PackedOut o,
@@ -201,19 +177,22 @@ __global__ void __launch_bounds__(384, 1)
   }
   if (tid == 0) {
     mbar_init(bar(C::kBarQFull), 1);
-    mbar_init(bar(C::kBarQEmpty), 1);
+    mbar_init(bar(C::kBarQEmpty), 2);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(bar(C::kBarFull + s), 1);
-      mbar_init(bar(C::kBarEmpty + s), 1);
+      mbar_init(bar(C::kBarEmpty + s), 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar(C::kBarS + i), 1);
       mbar_init(bar(C::kBarP + i), 128);
-      mbar_init(bar(C::kBarP + 2 + i), 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::kBarPV + i), 1);
       mbar_init(bar(C::kBarO + i), 1);
       mbar_init(bar(C::kBarOFree + i), 128);
     }
     mbar_init(bar(C::kBarTeardown), 1);
+    mbar_init(bar(C::kBarTeardown + 1), 1);
     fence_mbar_init();
     *abort = 0;
   }
@@ -243,8 +222,6 @@ __global__ void __launch_bounds__(384, 1)
   };
   auto aborted = [&]() -> bool { return __any_sync(0xffffffffu, *abort != 0); };
 
-  if (warp < 4) {
-  regs_shrink<C::kRegsOther>();
   if (warp == 0) {
     // ======================= copies ============================================
     const int page_rows = PAGED ? min(cache.page_size, kKeyTile) : kKeyTile;
@@ -306,26 +283,28 @@ __global__ void __launch_bounds__(384, 1)
       for (int i = max(slot - C::kStages, 0); i < slot; ++i)
         uwait(bar(C::kBarFull + i % C::kStages), (i / C::kStages) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 10) {
     // ======================= products ==========================================
     constexpr bool kBf = Half16<T>::kBf16;
-    constexpr uint32_t kIdS = idesc_16_f32<kBf>(128, 128, 0, 0);
+    constexpr uint32_t kIdS = idesc_16_f32<kBf>(128, 64, 0, 0);
     constexpr uint32_t kIdO = idesc_16_f32<kBf>(128, D, 0, 1);
     auto step = [](int k) -> uint64_t {   // K step of a K-major operand: 32 bytes of a box row
       return (uint64_t)(((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4);
     };
+    const int i = warp == 1 ? 0 : 1;   // subtile
     int slot = 0, seg = 0;
-    int np[2] = {0, 0};      // P tiles waited for
-    int no[2] = {0, 0};      // segments that used O
-    // S_i of the tile whose K is in ring slot `ks`
-    auto issue_s = [&](int i, int ks) {
+    int np[2] = {0, 0};                // P of each half waited for
+    int no = 0;                        // segments that used O
+    // S_ih of the tile whose K is in ring slot `ks`
+    auto issue_s = [&](int h, int ks) {
       const uint64_t qd = smem_desc_sw128(sbase + C::kOffQ + i * C::kTileBytes, 16, 1024);
-      const uint64_t kd = smem_desc_sw128(sbase + C::kOffKV + (ks % C::kStages) * C::kTileBytes, 16, 1024);
+      const uint64_t kd =
+          smem_desc_sw128(sbase + C::kOffKV + (ks % C::kStages) * C::kTileBytes + h * 64 * 128, 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + C::kColS + 128 * i, qd + step(k), kd + step(k), kIdS, k > 0 ? 1u : 0u);
-        tc_commit(bar(C::kBarS + i));
+          mma_ss(tmem + C::kColS + 128 * i + 64 * h, qd + step(k), kd + step(k), kIdS, k > 0 ? 1u : 0u);
+        tc_commit(bar(C::kBarS + 2 * h + i));
       }
       __syncwarp();
     };
@@ -334,18 +313,23 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     };
     auto full = [&](int sl) { return uwait(bar(C::kBarFull + sl % C::kStages), (sl / C::kStages) & 1); };
-    // a segment: first tile, end, key positions of the request, tiles of each subtile
+    // a segment: first tile, end, key positions of the request, end of the subtile's halves
     struct Part {
-      int ta, tb, kv, nt[2];
+      int ta, tb, kv, nh;
     };
     auto take = [&](Part &x) -> bool {
       if (!w.next(p)) return false;
       x.ta = w.s.ta;
       x.tb = w.s.tb;
       x.kv = w.s.r.kv;
-      x.nt[0] = min(subtile(p, w.s, tq1, 0).nt, x.tb);
-      x.nt[1] = min(subtile(p, w.s, tq1, 1).nt, x.tb);
+      x.nh = min(subtile(p, w.s, tq1, i).nh, 2 * x.tb);
       return true;
+    };
+    // S of a segment's first tile
+    auto first_scores = [&](const Part &x, int ks) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (2 * x.ta + h < x.nh) issue_s(h, ks);
     };
     Part cur, nxt;
     bool have = take(cur), ok = true;
@@ -353,8 +337,7 @@ __global__ void __launch_bounds__(384, 1)
       ok = uwait(bar(C::kBarQFull), 0) && full(0);
       tc_fence_after();
       if (ok) {
-        if (cur.ta < cur.nt[0]) issue_s(0, 0);
-        if (cur.ta < cur.nt[1]) issue_s(1, 0);
+        first_scores(cur, 0);
         commit(C::kBarEmpty + 0);
         if (cur.ta + 1 == cur.tb) commit(C::kBarQEmpty);
       }
@@ -366,69 +349,59 @@ __global__ void __launch_bounds__(384, 1)
       }
       bool have_n = false;
       for (int t = cur.ta; t < cur.tb; ++t, slot += 2) {
-        // after P V of this tile comes S of the next one, which may be the next unit's first
         const bool last = t + 1 == cur.tb;
         bool have_v = false, have_k = false;
 #pragma unroll
-        for (int i = 0; ok && i < 2; ++i) {
-          const int nt = cur.nt[i];
-          if (t < nt) {
-            if (!uwait(bar(C::kBarP + i), np[i] & 1)) {
+        for (int h = 0; ok && h < 2; ++h) {
+          if (2 * t + h >= cur.nh) continue;
+          if (!uwait(bar(C::kBarP + 2 * h + i), np[h] & 1)) {
+            ok = false;
+            break;
+          }
+          ++np[h];
+          if (!have_v) {
+            have_v = true;
+            if (!full(slot + 1)) {
               ok = false;
               break;
             }
-            if (!have_v) {
-              have_v = true;
-              if (!full(slot + 1)) {
-                ok = false;
-                break;
+            const int live = cur.kv - t * kKeyTile;
+            if (live < kKeyTile) {
+              // rows past the sequence's last key may hold anything: zero, so that 0 x Inf or
+              // NaN never reaches a sum (both warps write the same zeros, each before its product)
+              const int z0 = max(live, 0);
+              unsigned char *v = smem + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes;
+              for (int e = lane; e < (kKeyTile - z0) * (D / 8); e += 32) {
+                const int row = z0 + e / (D / 8), ch = e % (D / 8);
+                *reinterpret_cast<uint4 *>(v + (ch >> 3) * C::kBoxBytes + row * 128 +
+                                           (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
               }
-              const int live = cur.kv - t * kKeyTile;
-              if (live < kKeyTile) {
-                // rows past the sequence's last key may hold anything: zero, so that 0 x Inf or
-                // NaN never reaches a sum
-                const int z0 = max(live, 0);
-                unsigned char *v = smem + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes;
-                for (int e = lane; e < (kKeyTile - z0) * (D / 8); e += 32) {
-                  const int row = z0 + e / (D / 8), ch = e % (D / 8);
-                  *reinterpret_cast<uint4 *>(v + (ch >> 3) * C::kBoxBytes + row * 128 +
-                                             (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async();
-                __syncwarp();
-              }
-            }
-            if (t == cur.ta) {
-              // the first product of a unit overwrites O: its rows have been read
-              if (no[i] > 0 && !uwait(bar(C::kBarOFree + i), (no[i] - 1) & 1)) {
-                ok = false;
-                break;
-              }
-              ++no[i];
-            }
-            const uint64_t vd = smem_desc_sw128(
-                sbase + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes, C::kBoxBytes, 1024);
-            // P's first 64 columns are multiplied while the rest are still being formed
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (h == 1 && !uwait(bar(C::kBarP + 2 + i), np[i] & 1)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int k = 4 * h; k < 4 * h + 4; ++k)
-                  mma_ts(tmem + C::kColO + D * i, tmem + C::kColS + 128 * i + 8 * k,
-                         vd + (uint64_t)((k * 2048) >> 4), kIdO, (t > cur.ta || k > 0) ? 1u : 0u);
-                if (h == 1 && t + 1 >= nt) tc_commit(bar(C::kBarO + i));
-              }
+              fence_proxy_async();
               __syncwarp();
             }
-            if (!ok) break;
-            ++np[i];
           }
-          if (t + 1 < nt) {
+          const bool first = t == cur.ta && h == 0;
+          if (first) {
+            // the first product of a unit overwrites O: its rows have been read
+            if (no > 0 && !uwait(bar(C::kBarOFree + i), (no - 1) & 1)) {
+              ok = false;
+              break;
+            }
+            ++no;
+          }
+          tc_fence_after();
+          const uint64_t vd = smem_desc_sw128(
+              sbase + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes, C::kBoxBytes, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(tmem + C::kColO + D * i, tmem + C::kColS + 128 * i + 64 * h + 8 * k,
+                     vd + (uint64_t)(((4 * h + k) * 2048) >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
+            tc_commit(bar(C::kBarPV + i));
+            if (2 * t + h + 1 == cur.nh) tc_commit(bar(C::kBarO + i));
+          }
+          __syncwarp();
+          if (2 * (t + 1) + h < cur.nh) {
             if (!have_k) {
               have_k = true;
               if (!full(slot + 2)) {
@@ -437,12 +410,17 @@ __global__ void __launch_bounds__(384, 1)
               }
               tc_fence_after();
             }
-            issue_s(i, slot + 2);
+            issue_s(h, slot + 2);
           }
         }
         if (!ok) break;
+        // (slots that this subtile had no use for are given back once they have come)
+        if ((!have_v && !full(slot + 1)) || (!last && !have_k && !full(slot + 2))) {
+          ok = false;
+          break;
+        }
         commit(C::kBarEmpty + (slot + 1) % C::kStages);
-        // (after P V of both subtiles: the next unit's Q may still be on its way)
+        // (after P V of both halves: the next unit's Q may still be on its way)
         if (last) have_n = take(nxt);
         const bool more = !last || have_n;
         if (last && have_n) {
@@ -451,8 +429,7 @@ __global__ void __launch_bounds__(384, 1)
             break;
           }
           tc_fence_after();
-          if (nxt.ta < nxt.nt[0]) issue_s(0, slot + 2);
-          if (nxt.ta < nxt.nt[1]) issue_s(1, slot + 2);
+          first_scores(nxt, slot + 2);
         }
         if (more) {
           commit(C::kBarEmpty + (slot + 2) % C::kStages);
@@ -467,21 +444,20 @@ __global__ void __launch_bounds__(384, 1)
     if (!ok) {
       *abort = 1;
       // every product issued so far must finish before TMEM is released
-      commit(C::kBarTeardown);
-      uwait(bar(C::kBarTeardown), 0);
+      commit(C::kBarTeardown + i);
+      uwait(bar(C::kBarTeardown + i), 0);
     }
-  }
   } else {
     // ======================= softmax ===========================================
-    regs_grow<C::kRegsSoftmax>();
-    const int i = (warp - 4) >> 2;             // subtile
+    const int i = (warp - 2) >> 2;             // subtile
     const int sp = warp & 3;                   // TMEM sub-partition of this warp
     const int row = sp * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(sp * 32) << 16);
     const uint32_t s_addr = lane_addr + C::kColS + 128 * i, o_addr = lane_addr + C::kColO + D * i;
     const float sl2 = scale * kLog2e;
-    unsigned char *stage = smem + C::kOffStage + (warp - 4) * 4096;
-    int ns = 0, no = 0;
+    unsigned char *stage = smem + C::kOffStage + (warp - 2) * 4096;
+    int ns[2] = {0, 0};      // S of each half waited for
+    int nv = 0, no = 0;      // halves worked on, segments that used O
     bool ok = true;
     while (ok && w.next(p)) {
       const PackedSegment s = w.s;
@@ -490,19 +466,29 @@ __global__ void __launch_bounds__(384, 1)
       // keys this row sees: positions below lim (rows past the tile's go along with the last one)
       const int ltok = min(tok, s.r.n - 1);
       const int lim = p.causal ? max(min(s.r.past + ltok + 1, s.r.kv), 0) : s.r.kv;
-      const int t1 = min(x.nt, s.tb);
+      const int nh = min(x.nh, 2 * s.tb);
       float m_run = -INFINITY, l_run = 0.f;
-      for (int t = s.ta; t < t1; ++t, ++ns) {
-        if (!uwait(bar(C::kBarS + i), ns & 1)) {
+      for (int u = 2 * s.ta; u < nh; ++u, ++nv) {
+        const int h = u & 1;
+        if (!uwait(bar(C::kBarS + 2 * h + i), (h ? ns[1] : ns[0]) & 1)) {
           ok = false;
           break;
         }
+        ns[0] += h == 0;
+        ns[1] += h;
         tc_fence_after();
-        softmax_tile<T, D, ROUNDED>(s_addr, o_addr, sl2, lim - t * kKeyTile, bar(C::kBarP + i), m_run, l_run);
+        // the product of the half before: the one before that came before this S
+        auto pv_done = [&]() { return uwait(bar(C::kBarPV + i), (nv - 1) & 1); };
+        if (!softmax_half<T, D, ROUNDED>(s_addr + 64 * h, o_addr, sl2, lim - u * 64, pv_done, m_run, l_run)) {
+          ok = false;
+          break;
+        }
+        tc_fence_before();
+        mbar_arrive(bar(C::kBarP + 2 * h + i));
       }
       if (!ok) break;
       // ---- epilogue of the segment ----------------------------------------------
-      const bool used = s.ta < t1;
+      const bool used = 2 * s.ta < nh;
       if (used) {
         if (aborted() || !uwait(bar(C::kBarO + i), no & 1)) {
           ok = false;
@@ -561,7 +547,7 @@ __global__ void __launch_bounds__(384, 1)
           }
         }
       }
-      if (!whole && s.ta == 0 && tid == 128) cuts[blockIdx.x] = packed_cut(p, *start, s, gridDim.x);
+      if (!whole && s.ta == 0 && tid == 64) cuts[blockIdx.x] = packed_cut(p, *start, s, gridDim.x);
     }
     if (!ok) *abort = 1;
   }

@@ -23,15 +23,6 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
 // Programmatic dependent launch: the next kernel of the stream may be set up from here on; and
 // wait until the kernels before this one are complete and their writes are seen.  Every kernel
 // that launch_after starts waits before it touches global memory, and reads what kernels before
@@ -48,15 +39,6 @@ __device__ __forceinline__ int ld_int(const int32_t *p) {
 // generic-proxy writes to shared memory, made visible to the tensor cores and TMA
 __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Registers a thread, from here on; every warp of a warpgroup (four warps, the first a
-// multiple of four).  The shares of a CTA's warpgroups add up to what it was launched with.
-template <int N> __device__ __forceinline__ void regs_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N> __device__ __forceinline__ void regs_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // kind::f16 instruction descriptor with f16 or bf16 A and B, f32 accumulator

@@ -16,7 +16,8 @@
 // divisions, took 4 us at the start of every kernel.)
 // A unit counts unit_cost positions more than it has, for what its start and its
 // end take: without, a CTA that got many short units ran twice as long as the
-// others.  A cut that falls into these is one at the unit's start.
+// others.  A cut that falls into these is one at the unit's start, and one in a
+// short unit moves to its nearer end.
 // A unit inside one range is written by its CTA.  A unit cut by a range's end
 // leaves float32 partial sums, and packed_combine_kernel joins them in ascending
 // CTA order (no atomics: the same inputs give the same bits).
@@ -40,6 +41,7 @@ struct PackedProblem {
   int max_kv;               // most key positions a sequence can have (table width x page size)
   int unit_cost;            // what a unit takes beside its positions, in positions
   int min_range;            // no range is shorter than this, at least a tile
+  int whole;                // units of this many positions or fewer are not cut
 };
 
 struct PackedRequest {
@@ -227,8 +229,9 @@ template <class Cost> struct PackedWalk {
     len = Cost::length(p, s.r.n, s.r.kv, s.rt);
     s.nt = packed_tiles(len);
   }
-  // tiles that lie before position x of a unit
-  static __device__ __forceinline__ int tiles_before(const PackedProblem &p, int x) {
+  // tiles of the unit that lie before its position x
+  __device__ __forceinline__ int tiles_before(const PackedProblem &p, int x) const {
+    if (len <= p.whole) return 2 * x < len + p.unit_cost ? 0 : s.nt;
     return x <= p.unit_cost ? 0 : packed_tiles(x - p.unit_cost);
   }
   __device__ __forceinline__ bool next(const PackedProblem &p) {

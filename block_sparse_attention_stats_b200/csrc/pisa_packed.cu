@@ -47,10 +47,13 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
   using C = AttendCfg<D>;
   const int tq1 = 128 / p.G;
   p.tq = 2 * tq1;
-  // a unit's start and end take about three tiles, four with the float32 output (measured at 2 / 2.5 / 3 /
-  // 3.5: 964 / 899 / 882 / 876 us on 12000 + 700 + 4608 tokens, 126 / 128 / 127 / 132 us on 16 x 1000)
-  p.unit_cost = (ROUNDED ? 4 : 3) * kKeyTile;
+  // what a unit's start and end take, in tiles (measured at 1.5 / 2 / 2.5 / 3 / 4: 858 / 864 / 868 / 875 / 883
+  // us on 12000 + 700 + 4608 tokens, 98 / 99 / 100 / 99 / 102 us on 16 x 1000; with the float32 output 2317 /
+  // 2272 / 2252 / - / 2253 us a training step on 8192 + 4608 + 1500).  Cutting a unit of four tiles costs more
+  // than it balances: 13.8 against 11.5 us on seven prompts of up to 200 tokens
+  p.unit_cost = ROUNDED ? 3 * kKeyTile : 3 * kKeyTile / 2;
   p.min_range = p.unit_cost + kKeyTile;
+  p.whole = 4 * kKeyTile;
   CUtensorMap mq;
   PISA_TRY(map_query(&mq, q, Half16<T>::kBf16, D, p.G, p.T, p.Hkv, tq1));
   const PackedScratch s = packed_scratch(D, C::kRows);
@@ -71,6 +74,7 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
   p.tq = R / p.G;
   p.unit_cost = 3 * kKeyTile / 2;
   p.min_range = kKeyTile;
+  p.whole = 0;
   const PackedScratch s = packed_scratch(D, R);
   PackedCut *cuts = (PackedCut *)(ws + s.cuts);
   float *part = (float *)(ws + s.part);
