@@ -16,18 +16,23 @@
 // half as much shared memory, and the ring has six tiles instead of four (with
 // four, K of the next tile arrived 600 cycles late).  dk, dv have two accumulators
 // and no TMEM left: their pair stays in shared memory.
-// Roles (320 threads): warp 0 copies; warp 1 issues every product; warps 2-5
-// take columns 0 .. 63 of each 128 x 128 tile, warps 6-9 columns 64 .. 127, one
-// thread a row (TMEM lane).
-// The order of products keeps the tensor cores busy while the tile's weights are
-// formed, without a second pair of accumulators:
-//   dq      S_0 dP_0 | S_u+1 (once S_u is in registers), dQ += dS_u K_u, dP_u+1 | ...
-//   dk, dv  S_0 dP_0 | dV += P_u dout_u, S_u+1, dK += dS_u Q_u, dP_u+1 | ...
-// so the exponentials of tile u + 1 overlap dQ_u and dP_u+1 (dK_u and dP_u+1),
-// and dS_u overlaps S_u+1.  16-bit dS is written over the dP columns it was
-// formed from, 16-bit P over its S columns, each warpgroup over its own (the A
-// operand of the next product reads each half where it lies).  An overwrite is
-// safe because one thread issues all products and they run in order.
+// Roles (352 threads): warp 0 copies; warps 1 and 10 issue the products; warps 2-5
+// take columns 0 .. 63 of each 128 x 128 tile (half 0), warps 6-9 columns 64 .. 127
+// (half 1), one thread a row (TMEM lane).
+// The halves go their own ways, in this order each (h: half, u: tile):
+//   dq      warp 1: S_uh as soon as S_u-1,h is in registers
+//           warp 10: dQ += dS_uh K_uh, then dP_u+1,h
+//   dk, dv  warp 1: dV += P_uh dout_uh, then S_u+1,h
+//           warp 10: dK += dS_uh Q_uh, then dP_u+1,h
+// so one half's products run while the other half's weights are formed, and one
+// product's warp does not wait for the other product's operands.  Measured against
+// whole tiles with one issuing warp: 214 against 236 us at d = 64 (4096 + 2048 tokens,
+// 16 / 4 heads); at d = 128 level (1931 / 1938 us on 8192 + 4608 + 1500 tokens, 24 / 8
+// heads, in a loop at the 1 kW cap, where the halves' narrower products read more
+// shared memory).
+// 16-bit dS is written over the dP columns it was formed from, 16-bit P over its S
+// columns.  An overwrite is safe because the product that reads and the one that
+// overwrites come from one thread, whose products run in order.
 // Rounding: P and dS are rounded to bf16 for their products (the tensor cores
 // take no more), everything else is float32.
 #pragma once
@@ -70,7 +75,7 @@ __global__ void __launch_bounds__(256)
 }
 
 template <int D, bool KV> struct PackedBwdCfg {
-  static constexpr int kThreads = 320;
+  static constexpr int kThreads = 352;
   static constexpr int kRows = 128;
   static constexpr int kStages = D == 128 ? (KV ? 4 : 6) : (KV ? 8 : 12);
   static constexpr int kTileBytes = 128 * D * 2;
@@ -83,9 +88,10 @@ template <int D, bool KV> struct PackedBwdCfg {
   static constexpr int kOffMisc = kOffVec + kVecs * 1024;
   static constexpr int kSmem = kOffMisc + 1024 + 1024;     // + alignment slack
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // kBarAFull: the resident pair is in shared memory (KV) or in TMEM; kBarAEmpty: KV only
-  static constexpr int kBarAFull = 0, kBarAEmpty = 1, kBarS = 2, kBarDP = 3, kBarP = 4, kBarZ = 5, kBarAcc = 6,
-                       kBarAccFree = 7, kBarTeardown = 8, kBarFull = 9, kBarEmpty = kBarFull + kStages;
+  // kBarAFull: the resident pair is in shared memory (KV) or in TMEM; kBarAEmpty: KV only.  S, dP, P
+  // (dq: S is in registers) and Z (dS): + half
+  static constexpr int kBarAFull = 0, kBarAEmpty = 1, kBarS = 2, kBarDP = 4, kBarP = 6, kBarZ = 8, kBarAcc = 10,
+                       kBarAccFree = 11, kBarTeardown = 12, kBarFull = 14, kBarEmpty = kBarFull + kStages;
   static_assert(kBarEmpty + kStages <= 48, "barrier slots");
   static constexpr uint32_t kTmemCols = 512, kColS = 0, kColDP = 128, kColAcc = 256, kColA = 384;
 };
@@ -95,7 +101,7 @@ template <int D, bool KV> struct PackedBwdCfg {
 // KV = true: dk, dv.  The unit's rows are 128 keys, streamed pairs are Q and dout
 // of 128 tokens of one query head; tiles run over the heads, then the tokens.
 template <int D, bool KV>
-__global__ void __launch_bounds__(320, 1)
+__global__ void __launch_bounds__(352, 1)
     packed_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const PackedProblem p, float scale, const float *lse2, const float *delta,
@@ -126,13 +132,21 @@ __global__ void __launch_bounds__(320, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i <= C::kBarTeardown; ++i)
-      mbar_init(bar(i), i == C::kBarP || i == C::kBarZ || i == C::kBarAccFree || (!KV && i == C::kBarAFull)
-                            ? 256
-                            : 1);
+    mbar_init(bar(C::kBarAFull), KV ? 1 : 256);
+    mbar_init(bar(C::kBarAEmpty), 2);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(bar(C::kBarS + h), 1);
+      mbar_init(bar(C::kBarDP + h), 1);
+      mbar_init(bar(C::kBarP + h), 128);
+      mbar_init(bar(C::kBarZ + h), 128);
+      mbar_init(bar(C::kBarTeardown + h), 1);
+    }
+    mbar_init(bar(C::kBarAcc), KV ? 2 : 1);
+    mbar_init(bar(C::kBarAccFree), 256);
     for (int s = 0; s < kStages; ++s) {
+      // dq: K (even slots) is read for S and for dQ, V for dP; dk, dv: Q for S and for dK, dout for dP and dV
       mbar_init(bar(C::kBarFull + s), 1);
-      mbar_init(bar(C::kBarEmpty + s), 1);
+      mbar_init(bar(C::kBarEmpty + s), KV || s % 2 == 0 ? 2 : 1);
     }
     fence_mbar_init();
     *abort = 0;
@@ -264,9 +278,9 @@ __global__ void __launch_bounds__(320, 1)
       for (int i = max(slot - kStages, 0); i < slot; ++i)
         uwait(bar(C::kBarFull + i % kStages), (i / kStages) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 10) {
     // ======================= products ==========================================
-    constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t kIdS = idesc_bf16_f32(128, 64, 0, 0);
     constexpr uint32_t kIdAcc = idesc_bf16_f32(128, D, 0, 1);
     auto step = [](int k) -> uint64_t {
       return (uint64_t)(((k >> 2) * C::kBoxBytes + (k & 3) * 32) >> 4);
@@ -293,31 +307,36 @@ __global__ void __launch_bounds__(320, 1)
       tc_fence_after();
       return true;
     };
-    // S (x = 0) or dP (x = 1) of the tile whose pair starts at ring slot sl
-    auto issue_s = [&](int x, int sl) {
-      const uint64_t ad = smem_desc_sw128(sbase + C::kOffA + x * C::kTileBytes, 16, 1024);
-      const uint64_t bd = smem_desc_sw128(ring(sl + x), 16, 1024);
+    // warp 1 (x = 0): S, and dV of what is laid over it; warp 10 (x = 1): dP, and dK or dQ
+    const int x = warp == 1 ? 0 : 1;
+    const bool reads = KV || x == 1;
+    const uint32_t col = x ? C::kColDP : C::kColS;
+    const uint32_t acc = tmem + C::kColAcc + (KV && x == 0 ? D : 0);   // dQ or dK, dV after it
+    const int own = x, other = KV ? 1 - x : 0;   // slots of the pair: for S or dP, for the accumulator
+    const uint64_t ad = smem_desc_sw128(sbase + C::kOffA + x * C::kTileBytes, 16, 1024);
+    // half h of S or dP from ring slot sl
+    auto issue_s = [&](int h, int sl) {
+      const uint64_t bd = smem_desc_sw128(ring(sl) + h * 64 * 128, 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           if (KV)
-            mma_ss(tmem + (x ? C::kColDP : C::kColS), ad + step(k), bd + step(k), kIdS, k > 0 ? 1u : 0u);
+            mma_ss(tmem + col + 64 * h, ad + step(k), bd + step(k), kIdS, k > 0 ? 1u : 0u);
           else
-            mma_ts(tmem + (x ? C::kColDP : C::kColS), tmem + C::kColA + 64 * x + 8 * k, bd + step(k), kIdS,
-                   k > 0 ? 1u : 0u);
+            mma_ts(tmem + col + 64 * h, tmem + C::kColA + 64 * x + 8 * k, bd + step(k), kIdS, k > 0 ? 1u : 0u);
         }
-        tc_commit(bar(x ? C::kBarDP : C::kBarS));
+        tc_commit(bar((x ? C::kBarDP : C::kBarS) + h));
       }
       __syncwarp();
     };
-    // accumulator `a` += 16-bit tile at TMEM column `col` (two 64-wide halves) times ring slot sl
-    auto issue_acc = [&](int a, uint32_t col, int sl, bool first) {
-      const uint64_t bd = smem_desc_sw128(ring(sl), C::kBoxBytes, 1024);
+    // the accumulator += 16-bit half h times rows 64 h .. 64 h + 63 of ring slot sl
+    auto issue_acc = [&](int h, int sl, bool first) {
+      const uint64_t bd = smem_desc_sw128(ring(sl) + h * 64 * 128, C::kBoxBytes, 1024);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts(tmem + C::kColAcc + D * a, tmem + col + (k >> 2) * 64 + (k & 3) * 8,
-                 bd + (uint64_t)((k * 2048) >> 4), kIdAcc, (!first || k > 0) ? 1u : 0u);
+        for (int k = 0; k < 4; ++k)
+          mma_ts(acc, tmem + col + 64 * h + 8 * k, bd + (uint64_t)((k * 2048) >> 4), kIdAcc,
+                 (!first || k > 0) ? 1u : 0u);
       }
       __syncwarp();
     };
@@ -335,72 +354,67 @@ __global__ void __launch_bounds__(320, 1)
         // Q and dout are in TMEM: their ring slots are free
         if (elect_one()) {
           mbar_arrive(bar(C::kBarEmpty + slot % kStages));
-          mbar_arrive(bar(C::kBarEmpty + (slot + 1) % kStages));
+          if (x) mbar_arrive(bar(C::kBarEmpty + (slot + 1) % kStages));
         }
         __syncwarp();
         slot += 2;
       }
-      if (!take(slot, live(s.ta))) {
-        ok = false;
-        break;
+      int lv = live(s.ta);
+      for (int h = 0; ok && h < 2; ++h) {
+        // S of dq's first tile overwrites scores that the unit before has read
+        if ((!KV && x == 0 && u > 0 && !uwait(bar(C::kBarP + h), (u - 1) & 1)) ||
+            (h == 0 && !take(slot + own, lv))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        issue_s(h, slot + own);
       }
-      issue_s(0, slot);
-      if (!take(slot + 1, live(s.ta))) {
-        ok = false;
-        break;
-      }
-      issue_s(1, slot);
-      if (!KV) commit(C::kBarEmpty + (slot + 1) % kStages);
+      if (!ok) break;
+      commit(C::kBarEmpty + (slot + own) % kStages);
       if (KV && s.ta + 1 == s.tb) commit(C::kBarAEmpty);
-      for (int t = s.ta; t < s.tb; ++t, slot += 2, ++u) {
+      for (int t = s.ta; ok && t < s.tb; ++t, slot += 2, ++u) {
         const bool more = t + 1 < s.tb, first = t == s.ta;
-        // P_u of dk, dv is in TMEM; S_u of dq is in registers
-        if (aborted() || !uwait(bar(C::kBarP), u & 1)) {
-          ok = false;
-          break;
-        }
-        // the accumulators of the unit before have been read
-        if (first && seg > 0 && !uwait(bar(C::kBarAccFree), (seg - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (KV) {
-          issue_acc(1, C::kColS, slot + 1, first);            // dV += P dout
-          commit(C::kBarEmpty + (slot + 1) % kStages);
-        }
-        if (more) {
-          if (!take(slot + 2, live(t + 1))) {
-            ok = false;
-            break;
+        const int lnext = more ? live(t + 1) : 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (reads) {
+            if ((h == 0 && !take(slot + other, lv)) ||
+                !uwait(bar((x ? C::kBarZ : C::kBarP) + h), u & 1) ||
+                // the accumulators of the unit before have been read
+                (first && h == 0 && seg > 0 && !uwait(bar(C::kBarAccFree), (seg - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_acc(h, slot + other, first && h == 0);
+            if (h == 1) {
+              commit(C::kBarEmpty + (slot + other) % kStages);
+              if (!more) commit(C::kBarAcc);
+            }
           }
-          issue_s(0, slot + 2);
-        }
-        if (!uwait(bar(C::kBarZ), u & 1)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        issue_acc(0, C::kColDP, slot, first);                 // dQ += dS K, or dK += dS Q
-        commit(C::kBarEmpty + slot % kStages);
-        if (more) {
-          if (!take(slot + 3, live(t + 1))) {
-            ok = false;
-            break;
+          if (more) {
+            if ((!reads && !uwait(bar(C::kBarP + h), u & 1)) ||    // S_uh is in registers
+                (h == 0 && !take(slot + 2 + own, lnext))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue_s(h, slot + 2 + own);
+            if (h == 1) {
+              commit(C::kBarEmpty + (slot + 2 + own) % kStages);
+              if (KV && t + 2 == s.tb) commit(C::kBarAEmpty);
+            }
           }
-          issue_s(1, slot + 2);
-          if (!KV) commit(C::kBarEmpty + (slot + 3) % kStages);
-          if (KV && t + 2 == s.tb) commit(C::kBarAEmpty);
-        } else {
-          commit(C::kBarAcc);
         }
+        lv = lnext;
       }
       ++seg;
     }
     if (!ok) {
       *abort = 1;
-      commit(C::kBarTeardown);
-      uwait(bar(C::kBarTeardown), 0);
+      commit(C::kBarTeardown + x);
+      uwait(bar(C::kBarTeardown + x), 0);
     }
   } else {
     // ======================= weights ===========================================
@@ -413,8 +427,7 @@ __global__ void __launch_bounds__(320, 1)
     unsigned char *stage = smem + C::kOffStage + (warp - 2) * 2048;
     int u = 0, seg = 0, slot = 0;
     // this thread's row of Q (warpgroup 0) or dout (warpgroup 1) from the ring slots of segment
-    // w.s into TMEM, as packed pairs.  The products that read the pair before have completed: this
-    // thread has waited for the last S and dP
+    // w.s into TMEM, as packed pairs, once no product reads the pair before
     auto load_pair = [&]() -> bool {
       const int sl = slot + gw;
       if (!uwait(bar(C::kBarFull + sl % kStages), (sl / kStages) & 1)) return false;
@@ -460,7 +473,7 @@ __global__ void __launch_bounds__(320, 1)
         } else {
           c1 = (p.causal ? min(tok, s.r.n - 1) + 1 : s.r.n) - row0 - 64 * gw;
         }
-        if (aborted() || !uwait(bar(C::kBarS), u & 1)) {
+        if (!uwait(bar(C::kBarS + gw), u & 1)) {
           ok = false;
           break;
         }
@@ -476,7 +489,7 @@ __global__ void __launch_bounds__(320, 1)
         }
         if (!KV) {
           tc_fence_before();
-          mbar_arrive(bar(C::kBarP));          // S may be overwritten
+          mbar_arrive(bar(C::kBarP + gw));          // S may be overwritten
         }
         if (KV) {
           // (the slot's arrival also hands over lse and Delta)
@@ -507,9 +520,9 @@ __global__ void __launch_bounds__(320, 1)
           tmem_st_x32(s_addr, pk);
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(bar(C::kBarP));
+          mbar_arrive(bar(C::kBarP + gw));
         }
-        if (aborted() || !uwait(bar(C::kBarDP), u & 1)) {
+        if (!uwait(bar(C::kBarDP + gw), u & 1)) {
           ok = false;
           break;
         }
@@ -532,14 +545,9 @@ __global__ void __launch_bounds__(320, 1)
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(bar(C::kBarZ));
+        mbar_arrive(bar(C::kBarZ + gw));
       }
       if (!ok) break;
-      have = w.next(p);
-      if (!KV && have && !load_pair()) {
-        ok = false;
-        break;
-      }
       // ---- epilogue: dq = s dQ (half of the columns a warpgroup); dk = s dK, dv = dV (one each) ----
       if (aborted() || !uwait(bar(C::kBarAcc), seg & 1)) {
         ok = false;
@@ -547,6 +555,13 @@ __global__ void __launch_bounds__(320, 1)
       }
       ++seg;
       tc_fence_after();
+      // every product of the unit is done: the next one's pair may take TMEM, and its S and dP run
+      // while this unit's rows are stored
+      have = w.next(p);
+      if (!KV && have && !load_pair()) {
+        ok = false;
+        break;
+      }
       const bool whole = s.whole();
       constexpr int kCols = KV ? D : D / 2;
       const int col0 = KV ? 0 : gw * (D / 2);

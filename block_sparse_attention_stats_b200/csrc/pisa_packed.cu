@@ -52,7 +52,7 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
   // 2272 / 2252 / - / 2253 us a training step on 8192 + 4608 + 1500).  Cutting a unit of four tiles costs more
   // than it balances: 13.8 against 11.5 us on seven prompts of up to 200 tokens
   p.unit_cost = ROUNDED ? 3 * kKeyTile : 3 * kKeyTile / 2;
-  p.min_range = p.unit_cost + kKeyTile;
+  p.min_range = 3 * kKeyTile / 2;   // at most a unit a CTA where there are few
   p.whole = 4 * kKeyTile;
   CUtensorMap mq;
   PISA_TRY(map_query(&mq, q, Half16<T>::kBf16, D, p.G, p.T, p.Hkv, tq1));

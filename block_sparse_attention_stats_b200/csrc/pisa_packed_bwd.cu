@@ -48,7 +48,7 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
       lse2, delta));
   p.tq = 128 / p.G;
   p.unit_cost = 5 * kKeyTile / 2;
-  p.min_range = 4 * kKeyTile;
+  p.min_range = 3 * kKeyTile;
   p.whole = 4 * kKeyTile;
   CUtensorMap mq, mdo, mk, mv;
   PISA_TRY(map_query(&mq, q, true, D, p.G, p.T, p.Hkv, p.tq));
