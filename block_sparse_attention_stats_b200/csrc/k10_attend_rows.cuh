@@ -394,11 +394,12 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
           if (head_lane) {
             slot[row] = m[i][x];
             slot[R + row] = ls;
+            slot[2 * R + row] = ls;
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const int col = warp * (D / 8) + 8 * n + c2;
-            *reinterpret_cast<float2 *>(slot + 2 * R + ((size_t)(col >> 2) * R + row) * 4 + (col & 3)) =
+            *reinterpret_cast<float2 *>(slot + 3 * R + ((size_t)(col >> 2) * R + row) * 4 + (col & 3)) =
                 make_float2(acc[i][n][2 * x], acc[i][n][2 * x + 1]);
           }
         }

@@ -80,13 +80,14 @@ __device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedS
 // are visible.
 // A quarter of the exponentials as a polynomial on the multiply-add units did not
 // pay (918 against 893 us on 12000 + 700 + 4608 causal tokens).
-// ROUNDED (where the float32 output is wanted too): for the backward the sum takes
-// the rounded weights: dout_t . o_t is then the mean of dP under the weights
-// themselves, and does not lose dP - Delta to their rounding where one key holds
-// nearly all the weight.  Otherwise the sum keeps the float32 weights.
+// The sum is of the float32 weights.  ROUNDED (where the float32 output is wanted
+// too): for the backward the output is divided by the sum of the rounded weights:
+// dout_t . o_t is then the mean of dP under the weights themselves, and does not lose
+// dP - Delta to their rounding where one key holds nearly all the weight; lse still
+// comes from the float32 weights, summed beside.
 template <typename T, int D, bool ROUNDED, typename Wait>
 __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, float sl2, int seen, Wait pv_done,
-                                             float &m_run, float &l_run) {
+                                             float &m_run, float &l_run, float &e_run) {
   using namespace sm100;
   uint32_t r[64];
   tmem_ld_x32(s_addr, reinterpret_cast<uint32_t(&)[32]>(r[0]));
@@ -130,11 +131,13 @@ __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, f
       tmem_st_x32(o_addr + 32 * c, ov);
     }
     l_run *= f;
+    if (ROUNDED) e_run *= f;
   }
   if (grow) m_run = m_t;
   const float neg = m_run == -INFINITY ? 0.f : -m_run;   // no key seen yet: every weight is zero
   const float2 sl2x2 = make_float2(sl2, sl2), neg2 = make_float2(neg, neg);
   float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 exact[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   uint32_t pk[32];
 #pragma unroll
   for (int k = 0; k < 32; ++k) {
@@ -142,10 +145,15 @@ __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, f
     const float2 e = make_float2(ex2_approx(z.x), ex2_approx(z.y));
     pk[k] = Half16<T>::pack(e.x, e.y);
     acc[k & 1] = add2(acc[k & 1], ROUNDED ? Half16<T>::unpack(pk[k]) : e);
+    if (ROUNDED) exact[k & 1] = add2(exact[k & 1], e);
   }
   tmem_st_x32(s_addr, pk);
   const float2 a2 = add2(acc[0], acc[1]);
   l_run += a2.x + a2.y;
+  if (ROUNDED) {
+    const float2 e2 = add2(exact[0], exact[1]);
+    e_run += e2.x + e2.y;
+  }
   tmem_wait_st();
   return true;
 }
@@ -467,7 +475,7 @@ __global__ void __launch_bounds__(352, 1)
       const int ltok = min(tok, s.r.n - 1);
       const int lim = p.causal ? max(min(s.r.past + ltok + 1, s.r.kv), 0) : s.r.kv;
       const int nh = min(x.nh, 2 * s.tb);
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f, e_run = 0.f;
       for (int u = 2 * s.ta; u < nh; ++u, ++nv) {
         const int h = u & 1;
         if (!uwait(bar(C::kBarS + 2 * h + i), (h ? ns[1] : ns[0]) & 1)) {
@@ -479,7 +487,8 @@ __global__ void __launch_bounds__(352, 1)
         tc_fence_after();
         // the product of the half before: the one before that came before this S
         auto pv_done = [&]() { return uwait(bar(C::kBarPV + i), (nv - 1) & 1); };
-        if (!softmax_half<T, D, ROUNDED>(s_addr + 64 * h, o_addr, sl2, lim - u * 64, pv_done, m_run, l_run)) {
+        if (!softmax_half<T, D, ROUNDED>(s_addr + 64 * h, o_addr, sl2, lim - u * 64, pv_done, m_run, l_run,
+                                         e_run)) {
           ok = false;
           break;
         }
@@ -504,11 +513,13 @@ __global__ void __launch_bounds__(352, 1)
       const int prow = i * sub_rows + row;
       float *slot = part + ((size_t)blockIdx.x * 2 + s.slot()) * packed_slot_floats<D>(C::kRows);
       if (store) {
+        const float le = ROUNDED ? e_run : l_run;
         if (!whole) {
           slot[prow] = m_run;
           slot[C::kRows + prow] = l_run;
+          slot[2 * C::kRows + prow] = le;
         } else if (o.lse) {
-          o.lse[hr] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
+          o.lse[hr] = le == 0.f ? -INFINITY : (m_run + log2f(le)) * 0.6931471805599453f;
         }
       }
       if (used) {
@@ -517,7 +528,7 @@ __global__ void __launch_bounds__(352, 1)
         const long long at = (long long)head * o.head + (long long)token * o.row;
         // (a loop, not unrolled: units of a few tiles come back to this code often enough that its
         // length is paid for in instruction fetches)
-        float4 *ps = reinterpret_cast<float4 *>(slot + 2 * C::kRows) + prow;
+        float4 *ps = reinterpret_cast<float4 *>(slot + 3 * C::kRows) + prow;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ov[32];

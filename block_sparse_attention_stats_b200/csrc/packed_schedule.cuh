@@ -289,9 +289,9 @@ __device__ __forceinline__ PackedCut packed_cut(const PackedProblem &p, const Pa
   return c;
 }
 
-// partial slot: R rows of m and l, then the unnormalised output as [D / 4][R] float4
+// partial slot: R rows of m, l and the sum for lse, then the unnormalised output as [D / 4][R] float4
 template <int D> __host__ __device__ constexpr size_t packed_slot_floats(int R) {
-  return (size_t)R * (D + 2);
+  return (size_t)R * (D + 3);
 }
 
 template <typename T> struct Half16;
@@ -383,12 +383,12 @@ __global__ void __launch_bounds__(128)
   const int c0 = blockIdx.x, n = cut.last - c0 + 1;
   for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 16); e += gridDim.y * blockDim.x) {
     const int row = e % rows, c16 = e / rows;
-    float base = -INFINITY, l = 0.f, acc[16];
+    float base = -INFINITY, l = 0.f, le = 0.f, acc[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[j] = 0.f;
     // four partials at a time: their loads are in flight together
     for (int i0 = 0; i0 < n; i0 += 4) {
-      float m[4], ls[4];
+      float m[4], ls[4], es[4];
       float4 x[4][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -397,15 +397,17 @@ __global__ void __launch_bounds__(128)
         const float *s = part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot;
         m[k] = __ldcg(s + row);
         ls[k] = __ldcg(s + R + row);
+        es[k] = __ldcg(s + 2 * R + row);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          x[k][j] = __ldcg(reinterpret_cast<const float4 *>(s + 2 * R) + (size_t)(4 * c16 + j) * R + row);
+          x[k][j] = __ldcg(reinterpret_cast<const float4 *>(s + 3 * R) + (size_t)(4 * c16 + j) * R + row);
         if (i0 + k >= n) m[k] = -INFINITY;
       }
       const float top = fmaxf(fmaxf(base, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
       const float from = top == -INFINITY ? 0.f : top;
       const float f0 = exp2f(base - from);
       l *= f0;
+      le *= f0;
 #pragma unroll
       for (int j = 0; j < 16; ++j) acc[j] *= f0;
       base = top;
@@ -414,6 +416,7 @@ __global__ void __launch_bounds__(128)
         const float f = exp2f(m[k] - from);
         if (f == 0.f) continue;   // no weight (and, of a tile without keys, no output either)
         l = fmaf(f, ls[k], l);
+        le = fmaf(f, es[k], le);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           acc[4 * j] = fmaf(f, x[k][j].x, acc[4 * j]);
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(128)
       for (int j = 0; j < 4; ++j)
         reinterpret_cast<float4 *>(o.f32 + hr * D + 16 * c16)[j] =
             make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-    if (o.lse && c16 == 0) o.lse[hr] = l == 0.f ? -INFINITY : (base + log2f(l)) * 0.6931471805599453f;
+    if (o.lse && c16 == 0) o.lse[hr] = le == 0.f ? -INFINITY : (base + log2f(le)) * 0.6931471805599453f;
   }
 }
 

@@ -28,7 +28,7 @@ static PackedScratch packed_scratch(int d, int rows) {
   PackedScratch s;
   s.cuts = 0;
   s.part = align_up(kPackedCtas * sizeof(PackedCut), 256);
-  s.total = s.part + align_up((size_t)kPackedCtas * 2 * rows * (d + 2) * sizeof(float), 256);
+  s.total = s.part + align_up((size_t)kPackedCtas * 2 * rows * (d + 3) * sizeof(float), 256);
   return s;
 }
 

@@ -345,8 +345,9 @@ size_t pisa_varlen_attention_bwd_workspace_bytes(int T, int Hq, int Hkv, int d);
 /* Gradients of pisa_varlen_attention: given dout = dL/d out writes dq, dk, dv
  * (a key head's from every query head of its group).  bf16 only: dS = P (dP -
  * Delta) has no scale of its own and would underflow in f16.  lse and out_f32
- * from one forward call on the same inputs that was given both (its denominator
- * then sums the rounded weights, see pisa_sparse_attention_fwd).  dq, dk, dv
+ * from one forward call on the same inputs that was given both (its output is
+ * then divided by the sum of the rounded weights, which the backward needs; lse is
+ * the sum's before rounding either way).  dq, dk, dv
  * overlap no input and one another not. */
 pisa_status pisa_varlen_attention_bwd(pisa_rows q, pisa_rows k, pisa_rows v, pisa_rows dout,
                                       pisa_dtype dtype, const float *lse, const float *out_f32,
