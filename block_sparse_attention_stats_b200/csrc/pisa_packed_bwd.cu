@@ -94,7 +94,7 @@ pisa_status pisa_varlen_attention_bwd(pisa_rows q, pisa_rows k, pisa_rows v, pis
   if (B < 1 || T < 0 || Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv) return PISA_ERR_INVALID_ARG;
   if (dtype != PISA_BF16 && dtype != PISA_F16 && dtype != PISA_F32) return PISA_ERR_INVALID_ARG;
   if (dtype != PISA_BF16 || (d != 64 && d != 128)) return PISA_ERR_UNSUPPORTED;
-  if (Hq > 65535 || Hq / Hkv > 128 || T > (1 << 24) || B > (1 << 24)) return PISA_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hq / Hkv > 128 || T > (1 << 24) || B > (1 << 16)) return PISA_ERR_UNSUPPORTED;
   // a key tile's length, the 128-row tiles of its whole group, is counted in 32 bits
   if ((long long)ceil_div(T, 128) * 128 * (Hq / Hkv) > (1 << 30)) return PISA_ERR_UNSUPPORTED;
   if (!(scale >= 0.f) || !std::isfinite(scale) || (flags & ~(PISA_CAUSAL | PISA_ZERO_TAIL))) return PISA_ERR_INVALID_ARG;

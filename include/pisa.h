@@ -295,7 +295,8 @@ size_t pisa_dense_attention_workspace_bytes(int B, int H, int L, int d, pisa_dty
  *    behind the last sequence are neither read into any result nor written
  *    (unless PISA_ZERO_TAIL is set).
  *  - Query head h reads key head h / (Hq / Hkv); Hq is a multiple of Hkv, and
- *    Hq / Hkv at most 128.  d is 64 or 128.  dtype is PISA_BF16 or PISA_F16
+ *    Hq / Hkv at most 128.  d is 64 or 128.  B is at most 65536, T 2^24, a request
+ *    at most 2^30 positions long.  dtype is PISA_BF16 or PISA_F16
  *    (gradients: PISA_BF16); scores, maxima, sums and accumulators are float32,
  *    softmax weights are rounded to dtype for their product with the values.
  *  - Lengths, offsets and tables stay on the device: a captured call serves

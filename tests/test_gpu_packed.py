@@ -313,3 +313,65 @@ def test_nothing_to_do(P):
     assert (out == 0).all()
     assert all((g == 0).all() for g in torch.autograd.grad(out.float().sum(), (q, k, v)))
     P.pisa_device_status()
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_random_batches(P, seed):
+    """Batches of any shape: where ranges cut units differs from one to the next."""
+    import random
+    rng = random.Random(seed)
+    d = rng.choice([64, 128])
+    hkv = rng.choice([1, 2, 3])
+    hq = hkv * rng.choice([1, 2, 3, 5, 8])
+    longest = rng.choice([20, 150, 700])
+    lens = [rng.choice([0, 1, rng.randint(1, longest), longest]) for _ in range(rng.randint(1, 9))]
+    causal, T = rng.random() < 0.7, sum(lens) + 3
+    q, k, v, g = (rows(seed + i, h, T, d, BF, s) for i, h, s in ((1, hq, 1.5), (2, hkv, 1), (3, hkv, 1), (4, hq, 1)))
+    ref = U.varlen(q.double(), k.double(), v.double(), lens, causal, d ** -0.5, BF)
+    want, bound = U.varlen_grads(q.double(), k.double(), v.double(), g.double(), lens, causal, d ** -0.5, BF)
+    leaves = [x.cuda().requires_grad_() for x in (q, k, v)]
+    n = sum(lens)
+    lse, o32 = torch.zeros(hq, T, device="cuda"), torch.zeros(hq, T, d, device="cuda")
+    for f in (None, o32):                    # without and with the float32 output
+        out = P.pisa_varlen_attention(*(x.detach() for x in leaves), cu_of(lens), causal, lse=lse, out_f32=f)
+        U.check(out[:, :n], ref["out"][:, :n], ref["bound"][:, :n], "out")
+        U.check(lse[:, :n], ref["lse"][:, :n], ref["lse_bound"][:, :n], "lse")
+    U.check(o32[:, :n].to(BF), ref["out"][:, :n], ref["bound"][:, :n], "out_f32")
+    got = torch.autograd.grad(P.varlen_attention(*leaves, cu_of(lens), causal), leaves, g.cuda())
+    P.pisa_device_status()
+    for name, x in zip(("dq", "dk", "dv"), got):
+        U.check(x, want[name], bound[name], name)
+
+
+def test_backward_on_another_stream(P):
+    lens, d = [200, 31], 64
+    leaves = [rows(i, h, 231, d, BF).cuda().requires_grad_() for i, h in ((1, 4), (2, 2), (3, 2))]
+    g, cu = rows(4, 4, 231, d, BF).cuda(), cu_of(lens)
+    want = torch.autograd.grad(P.varlen_attention(*leaves, cu), leaves, g)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = torch.autograd.grad(P.varlen_attention(*leaves, cu), leaves, g)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_second_derivative_is_refused(P):
+    leaves = [rows(i, 2, 20, 64, BF).cuda().requires_grad_() for i in (1, 2, 3)]
+    out = P.varlen_attention(*leaves, cu_of([20]))
+    dq, = torch.autograd.grad(out.float().square().sum(), leaves[:1], create_graph=True)
+    with pytest.raises(RuntimeError):
+        dq.float().sum().backward()
+
+
+def test_out_may_not_be_an_input(P):
+    q, k, v = (rows(i, 2, 20, 64, BF).cuda() for i in (1, 2, 3))
+    for bad in (q, k, v):
+        with pytest.raises(P.PisaError):
+            P.pisa_varlen_attention(q, k, v, cu_of([20]), out=bad)
+    with pytest.raises(ValueError):
+        P.pisa_varlen_attention(q, k, v, cu_of([20]).cpu())
+    with pytest.raises(ValueError):
+        P.pisa_varlen_attention(q, k, v, cu_of([20]).long())
+    with pytest.raises(ValueError):
+        P.pisa_varlen_attention(q, k, v, cu_of([20]), lse=torch.zeros(2, 21, device="cuda"))

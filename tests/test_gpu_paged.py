@@ -382,3 +382,39 @@ def test_paged_repeats_bitwise_on_streams(P):
         torch.cuda.synchronize()
         assert all(torch.equal(x, want) for x in got)
     P.pisa_device_status()
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_random_requests(P, seed):
+    rng = random.Random(seed)
+    d, ps, dtype = rng.choice([64, 128]), rng.choice([16, 32, 64, 128, 256]), rng.choice([BF, HF])
+    hkv = rng.choice([1, 2, 5])
+    hq = hkv * rng.choice([1, 2, 3, 7, 16])
+    most = rng.choice([1, 4, 30, 200])
+    kv = [rng.choice([1, rng.randint(1, 40), rng.randint(1, 1500)]) for _ in range(rng.randint(1, 7))]
+    new = [rng.choice([0, 1, min(m, rng.randint(1, most))]) for m in kv]
+    new[rng.randrange(len(new))] = 1
+    q, kc, vc, dirty, table = paged_case(new, kv, hq, hkv, d, ps, dtype, seed)
+    want = U.paged(q.double(), kc.double(), vc.double(), table, new, kv, d ** -0.5, dtype)
+    lse = torch.zeros(hq, sum(new), device="cuda")
+    out = P.pisa_paged_attention(q.cuda(), dirty[0].cuda(), dirty[1].cuda(), i32(table), i32(U.offsets(new)), i32(kv),
+                                 lse=lse)
+    P.pisa_device_status()
+    U.check(out, want["out"], want["bound"], "out")
+    U.check(lse, want["lse"], want["lse_bound"], "lse")
+
+
+def test_a_prompt_in_the_cache_is_the_prompt(P):
+    """The same prompts through the packed call and through pages: the same numbers to rounding."""
+    new, hq, hkv, d, ps = [300, 45, 129], 6, 2, 128, 32
+    T = sum(new)
+    q, k, v = rows(1, hq, T, d), rows(2, hkv, T, d), rows(3, hkv, T, d)
+    a = P.pisa_varlen_attention(q.cuda(), k.cuda(), v.cuda(), i32(U.offsets(new)))
+    table = torch.full((3, 12), -1, dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros(40, hkv, ps, d, dtype=BF, device="cuda") for _ in range(2))
+    b, _ = P.pisa_paged_step(q.cuda(), k.cuda(), v.cuda(), kc, vc, i32([0] * 3), i32(new), table,
+                             i32(list(range(40))), i32([40]))
+    P.pisa_device_status()
+    want = U.varlen(q.double(), k.double(), v.double(), new, True, d ** -0.5, BF)
+    U.check(a, want["out"], want["bound"], "packed")
+    U.check(b, want["out"], want["bound"], "paged")

@@ -51,7 +51,8 @@ COMMON = [
     (dict(dtype=7), INVALID), (dict(dtype=L.PISA_F32), UNSUPPORTED),
     (dict(B=0), INVALID), (dict(T=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID),
     (dict(Hq=5), INVALID), (dict(Hq=258, Hkv=2), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(d=0), INVALID),
-    (dict(T=(1 << 24) + 1), UNSUPPORTED), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(T=(1 << 24) + 1), UNSUPPORTED), (dict(B=(1 << 16) + 1), UNSUPPORTED),
+    (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(scale=float("inf")), INVALID), (dict(cu=None), INVALID), (dict(cu=A[5] + 2), INVALID),
     (dict(q=R(None)), INVALID), (dict(q=R(A[0] + 8)), INVALID), (dict(q=R(A[0], r=60)), INVALID),
     (dict(q=R(A[0], r=68)), INVALID), (dict(q=R(A[0], h=0)), INVALID), (dict(q=R(A[0], h=-6400)), INVALID),
@@ -97,6 +98,7 @@ def bwd(lib, q=None, dout=None, dtype=L.PISA_BF16, lse=A[7], o32=A[8], cu=A[5], 
     (dict(dtype=L.PISA_F16), UNSUPPORTED), (dict(dtype=L.PISA_F32), UNSUPPORTED), (dict(dtype=9), INVALID),
     (dict(B=0), INVALID), (dict(Hq=5), INVALID), (dict(Hq=400), UNSUPPORTED), (dict(d=32), UNSUPPORTED),
     (dict(scale=-0.5), INVALID), (dict(flags=8), INVALID), (dict(cu=None), INVALID), (dict(lse=None), INVALID),
+    (dict(B=(1 << 16) + 1), UNSUPPORTED), (dict(T=1 << 24, Hq=128, Hkv=1), UNSUPPORTED),
     (dict(lse=A[7] + 2), INVALID), (dict(o32=None), INVALID), (dict(o32=A[8] + 4), INVALID),
     (dict(dout=R(A[3], r=8)), INVALID), (dict(dq=R(A[0])), INVALID), (dict(dk=R(A[9])), INVALID),
     (dict(dv=R(A[10])), INVALID), (dict(dq=R(A[8])), INVALID), (dict(dv=R(A[7])), INVALID),
