@@ -332,6 +332,11 @@ EncodeTiledFn encode_tiled() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
+  // the driver's function wants a current context, which a host thread (autograd's, say) only has
+  // after a runtime call that makes one
+  static thread_local bool ready = false;
+  int dev;
+  if (!ready && cudaGetDevice(&dev) == cudaSuccess) ready = cudaSetDevice(dev) == cudaSuccess;
   return fn;
 }
 

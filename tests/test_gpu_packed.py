@@ -1,6 +1,7 @@
 """Attention over packed sequences: the kernels against their 64-bit form, with the bounds of
 packed_util, at the lengths, heads, layouts and masks where they can go wrong."""
 import math
+import threading
 
 import pytest
 import torch
@@ -354,6 +355,50 @@ def test_backward_on_another_stream(P):
         got = torch.autograd.grad(P.varlen_attention(*leaves, cu), leaves, g)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("which", ["forward", "backward", "paged", "write"])
+def test_first_call_of_a_thread(P, which):
+    """Each thread has a current context of its own, and none before its first call."""
+    lens, d = [200, 31], 64
+    q, k, v, g = (rows(i, h, 231, d, BF).cuda() for i, h in ((1, 4), (2, 2), (3, 2), (4, 4)))
+    cu = cu_of(lens)
+    kc, vc = (rows(i, 20 * 2 * 16, 1, d, BF).cuda().view(20, 2, 16, d) for i in (5, 6))
+    table = torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10)
+    kv = torch.tensor([150, 29], dtype=torch.int32, device="cuda")
+    lse, o32 = torch.empty(4, 231, device="cuda"), torch.empty(4, 231, d, device="cuda")
+    out = P.pisa_varlen_attention(q, k, v, cu, lse=lse, out_f32=o32)
+    two = cu_of([1, 1])
+
+    def call():
+        if which == "forward":
+            return P.pisa_varlen_attention(q, k, v, cu, out=torch.empty_like(q)),
+        if which == "backward":
+            return P.pisa_varlen_attention_bwd(q, k, v, g, lse, o32, cu)
+        if which == "paged":
+            return P.pisa_paged_attention(q[:, :2], kc, vc, table, two, kv),
+        caches = torch.zeros_like(kc), torch.zeros_like(vc)
+        P.pisa_page_write(k, v, torch.arange(231, device="cuda"), *caches)
+        return caches
+
+    want = call()      # what it allocates is in the allocator's pool from here on
+    torch.cuda.synchronize()
+    got = []
+
+    def body():
+        try:
+            got.extend(call())
+            torch.cuda.synchronize()
+        except Exception as e:
+            got.append(e)
+
+    del out
+    worker = threading.Thread(target=body)
+    worker.start()
+    worker.join()
+    assert len(got) == len(want), got
+    for a, b in zip(got, want):
+        assert torch.is_tensor(a) and torch.equal(a, b), a
 
 
 def test_second_derivative_is_refused(P):
