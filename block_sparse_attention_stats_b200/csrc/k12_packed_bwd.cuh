@@ -612,31 +612,37 @@ __global__ void __launch_bounds__(352, 1)
   }
 }
 
+struct PackedSums {
+  PackedProblem p;
+  const PackedCut *cuts[2];      // of dq, and of dk and dv
+  const float *part[2];
+  __nv_bfloat16 *out[3];         // dq, dk, dv
+  long long head[3], row[3];
+  int clear;
+};
+
 // Joins the partial sums of the unit that CTA blockIdx.x's range cuts, in
-// ascending CTA order.  blockIdx.z: dk or dv (KV).
-template <int D, bool KV>
-__global__ void __launch_bounds__(128)
-    packed_sum_kernel(const PackedProblem p, const PackedCut *cuts, const float *part,
-                      __nv_bfloat16 *__restrict__ out0, long long out0_head, long long out0_row,
-                      __nv_bfloat16 *__restrict__ out1, long long out1_head, long long out1_row, int clear) {
+// ascending CTA order.  blockIdx.z: dq, dk or dv.
+template <int D> __global__ void __launch_bounds__(128) packed_sum_kernel(const PackedSums a) {
   sm100::allow_next_launch();
   sm100::wait_for_launches_before();
-  if (clear)
-    clear_tail<D>(p, KV ? p.Hkv : p.Hq, blockIdx.z ? out1 : out0, blockIdx.z ? out1_head : out0_head,
-                  blockIdx.z ? out1_row : out0_row,
+  const int z = blockIdx.z, kv = z > 0;
+  const PackedProblem &p = a.p;
+  __nv_bfloat16 *out = a.out[z];
+  const long long hs = a.head[z], rs = a.row[z];
+  if (a.clear)
+    clear_tail<D>(p, kv ? p.Hkv : p.Hq, out, hs, rs,
                   ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
                   (long long)gridDim.x * gridDim.y * blockDim.x);
-  const PackedCut cut = packed_cut_at(cuts, blockIdx.x);
+  const PackedCut cut = packed_cut_at(a.cuts[kv], blockIdx.x);
   if (!cut.valid) return;
   bool bad = false;
   const PackedRequest r = packed_request(p, cut.b, bad);
-  const int per = KV ? 128 : p.tq, g = KV ? 1 : p.G, tok0 = cut.rt * per;
+  const int per = kv ? 128 : p.tq, g = kv ? 1 : p.G, tok0 = cut.rt * per;
   const int rows = min(r.n - tok0, per) * g;
   const int c0 = blockIdx.x, n = cut.last - c0 + 1;
-  constexpr size_t kSlot = (size_t)(KV ? 2 : 1) * 128 * (D / 4);
-  const float4 *base = reinterpret_cast<const float4 *>(part) + blockIdx.z * (128 * (D / 4));
-  __nv_bfloat16 *out = blockIdx.z ? out1 : out0;
-  const long long hs = blockIdx.z ? out1_head : out0_head, rs = blockIdx.z ? out1_row : out0_row;
+  const size_t kSlot = (size_t)(kv ? 2 : 1) * 128 * (D / 4);
+  const float4 *base = reinterpret_cast<const float4 *>(a.part[kv]) + (z == 2 ? 128 * (D / 4) : 0);
   for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 16); e += gridDim.y * blockDim.x) {
     const int row = e % rows, c16 = e / rows;
     float acc[16];

@@ -18,17 +18,21 @@ namespace pisa {
 pisa_status take_packed_bwd_status(unsigned *bits) { return take_status_word(&g_device_status, bits); }
 
 struct PackedBwdLayout {
-  size_t lse2, delta, cuts, part, total;
+  size_t lse2, delta, cuts[2], part[2], total;   // cuts and partial sums of dq, and of dk and dv
 };
 static PackedBwdLayout packed_bwd_layout(int T, int Hq, int d) {
   PackedBwdLayout l;
   const size_t rows = align_up((size_t)Hq * T * sizeof(float), 256);
   l.lse2 = 0;
   l.delta = rows;
-  l.cuts = 2 * rows;
-  l.part = l.cuts + align_up(kPackedCtas * sizeof(PackedCut), 256);
-  // partial sums of dq, then of dk and dv (the two kernels run one after the other)
-  l.total = l.part + (size_t)kPackedCtas * 2 * 2 * 128 * d * sizeof(float);
+  size_t at = 2 * rows;
+  for (int i = 0; i < 2; ++i) {
+    l.cuts[i] = at;
+    at += align_up(kPackedCtas * sizeof(PackedCut), 256);
+    l.part[i] = at;
+    at += (size_t)kPackedCtas * 2 * (i + 1) * 128 * d * sizeof(float);
+  }
+  l.total = at;
   return l;
 }
 
@@ -40,16 +44,30 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
   using Cq = PackedBwdCfg<D, false>;
   using Ck = PackedBwdCfg<D, true>;
   const PackedBwdLayout l = packed_bwd_layout(p.T, p.Hq, D);
-  float *lse2 = (float *)(ws + l.lse2), *delta = (float *)(ws + l.delta), *part = (float *)(ws + l.part);
-  PackedCut *cuts = (PackedCut *)(ws + l.cuts);
+  float *lse2 = (float *)(ws + l.lse2), *delta = (float *)(ws + l.delta);
+  PackedSums s{};
+  const pisa_rows *out[3] = {&dq, &dk, &dv};
+  for (int i = 0; i < 3; ++i) {
+    s.out[i] = (__nv_bfloat16 *)out[i]->data;
+    s.head[i] = out[i]->head_stride;
+    s.row[i] = out[i]->row_stride;
+  }
+  PackedCut *cuts[2];
+  float *part[2];
+  for (int i = 0; i < 2; ++i) {
+    s.cuts[i] = cuts[i] = (PackedCut *)(ws + l.cuts[i]);
+    s.part[i] = part[i] = (float *)(ws + l.part[i]);
+  }
+  s.clear = clear;
   const long long rows = (long long)p.Hq * p.T;
-  PISA_TRY(launch_after(packed_delta_kernel<D>, dim3((unsigned)std::min<long long>((rows + 7) / 8, 148 * 8)), 256, 0, st, 
+  PISA_TRY(launch_after(packed_delta_kernel<D>, dim3((unsigned)std::min<long long>((rows + 7) / 8, 148 * 8)), 256, 0, st,
       (const __nv_bfloat16 *)dout.data, dout.head_stride, dout.row_stride, out_f32, lse, p.Hq, p.T, p.cu, p.B,
       lse2, delta));
   p.tq = 128 / p.G;
   p.unit_cost = 5 * kKeyTile / 2;
   p.min_range = 3 * kKeyTile;
   p.whole = 4 * kKeyTile;
+  s.p = p;
   CUtensorMap mq, mdo, mk, mv;
   PISA_TRY(map_query(&mq, q, true, D, p.G, p.T, p.Hkv, p.tq));
   PISA_TRY(map_query(&mdo, dout, true, D, p.G, p.T, p.Hkv, p.tq));
@@ -58,21 +76,16 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Cq::kSmem));
   PISA_TRY(launch_after(packed_bwd_kernel<D, false>, dim3(kPackedCtas), Cq::kThreads, Cq::kSmem, st, 
-      mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr,
-      0, 0, cuts, part));
-  PISA_TRY(launch_after(packed_sum_kernel<D, false>, dim3(kPackedCtas, D / 16), 128, 0, st, 
-      p, cuts, part, (__nv_bfloat16 *)dq.data, dq.head_stride, dq.row_stride, nullptr, 0, 0, clear));
+      mq, mdo, mk, mv, p, scale, lse2, delta, s.out[0], s.head[0], s.row[0], nullptr, 0, 0, cuts[0], part[0]));
   // dk, dv: Q and dout one head at a time
   PISA_TRY(map_rows(&mq, q, true, D, p.T, p.Hq, 128));
   PISA_TRY(map_rows(&mdo, dout, true, D, p.T, p.Hq, 128));
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Ck::kSmem));
   PISA_TRY(launch_after(packed_bwd_kernel<D, true>, dim3(kPackedCtas), Ck::kThreads, Ck::kSmem, st, 
-      mq, mdo, mk, mv, p, scale, lse2, delta, (__nv_bfloat16 *)dk.data, dk.head_stride, dk.row_stride,
-      (__nv_bfloat16 *)dv.data, dv.head_stride, dv.row_stride, cuts, part));
-  return launch_after(packed_sum_kernel<D, true>, dim3(kPackedCtas, D / 16, 2), 128, 0, st, 
-      p, cuts, part, (__nv_bfloat16 *)dk.data, dk.head_stride, dk.row_stride, (__nv_bfloat16 *)dv.data,
-      dv.head_stride, dv.row_stride, clear);
+      mq, mdo, mk, mv, p, scale, lse2, delta, s.out[1], s.head[1], s.row[1], s.out[2], s.head[2], s.row[2],
+      cuts[1], part[1]));
+  return launch_after(packed_sum_kernel<D>, dim3(kPackedCtas, D / 16, 3), 128, 0, st, s);
 }
 
 }  // namespace pisa
