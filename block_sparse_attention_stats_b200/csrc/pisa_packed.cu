@@ -61,8 +61,8 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
   float *part = (float *)(ws + s.part);
   PISA_CUDA(cudaFuncSetAttribute(attend_tc_kernel<T, D, PAGED, ROUNDED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem));
-  PISA_TRY(launch_after(attend_tc_kernel<T, D, PAGED, ROUNDED>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, mq, mk, mv, p, cache, scale, o,
-                                                                            cuts, part));
+  PISA_TRY(launch_after(attend_tc_kernel<T, D, PAGED, ROUNDED>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, mq, mk,
+                        mv, p, cache, scale, o, cuts, part));
   return launch_combine<T, D>(p, cuts, part, C::kRows, o, clear, st);
 }
 
@@ -72,6 +72,8 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
                                cudaStream_t st) {
   using C = RowsCfg<D, R>;
   p.tq = R / p.G;
+  // (at 1 / 1.5 / 2 tiles a unit: 158 / 152 / 149 us on 48 requests of 1 to 8000 keys, 957 MB; where
+  // units are short a larger count leaves CTAs idle)
   p.unit_cost = 3 * kKeyTile / 2;
   p.min_range = kKeyTile;
   p.whole = 0;
@@ -80,7 +82,7 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
   float *part = (float *)(ws + s.part);
   PISA_CUDA(cudaFuncSetAttribute(attend_rows_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem));
-  PISA_TRY(launch_after(attend_rows_kernel<T, D, R>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, 
+  PISA_TRY(launch_after(attend_rows_kernel<T, D, R>, dim3(kPackedCtas), C::kThreads, C::kSmem, st,
       mk, mv, p, cache, (const T *)q.data, q.head_stride, q.row_stride, scale, o, cuts, part));
   return launch_combine<T, D>(p, cuts, part, R, o, 0, st);
 }
@@ -100,18 +102,25 @@ template <typename T, int D>
 static pisa_status run_paged(const PackedProblem &p, const PagedKV &cache, const pisa_rows &q,
                              const pisa_pages &k, const pisa_pages &v, float scale, const PackedOut &o,
                              unsigned char *ws, cudaStream_t st) {
-  // rows of an average request (the lengths themselves are on the device; either kernel
-  // serves any of them)
-  const long long rows = ((long long)p.T * p.G + p.B - 1) / p.B;
-  const long long r = std::max<long long>(rows, p.G);
-  const bool few = r <= 32;
+  // Requests of up to 32 rows (tokens times the heads of a group) are for the kernel of few rows: 16
+  // requests of 8 tokens, 3 heads to a key head and 4000 keys take 61 / 62 us there and 73 / 59 with
+  // 128-row products (pages of 16 / 64), 48 of 5 tokens 138 / 127 and 188 / 141; requests of 33 to 64
+  // rows 97 - 101 and 79 - 80.  A longer one reads its keys once for every 32 rows there: 330 single
+  // tokens beside a chunk of 2900 took 3236 us, and 600 with 128-row products.
+  // The lengths are on the device, and either kernel serves any of them.  So what T and B say
+  // decides: T = k B is taken for k tokens a request, and other batches go to the kernel of few
+  // rows where the tokens beyond one a request, were they all one request's, make a quarter as
+  // many tiles as there are requests (48 single tokens beside a chunk of 100: 143 against 188 us).
+  const long long r = std::max<long long>(((long long)p.T * p.G + p.B - 1) / p.B, p.G);
+  const long long more = (long long)std::max(p.T - p.B, 0) * p.G;
+  const bool few = r <= 32 && (p.T % p.B == 0 || more <= 8ll * p.B);
   CUtensorMap mk, mv;
   const int halves = few ? D / 64 : 1;
   PISA_TRY(map_pages(&mk, k, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages, halves));
   PISA_TRY(map_pages(&mv, v, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages, halves));
+  if (!few) return launch_tc<T, D, true, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
   if (r <= 16) return launch_rows<T, D, 16>(p, cache, q, mk, mv, scale, o, ws, st);
-  if (few) return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
-  return launch_tc<T, D, true, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
+  return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
 }
 
 // ---- argument checks --------------------------------------------------------------------

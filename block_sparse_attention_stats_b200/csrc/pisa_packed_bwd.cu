@@ -75,14 +75,14 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
   PISA_TRY(map_rows(&mv, v, true, D, p.T, p.Hkv, 128));
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Cq::kSmem));
-  PISA_TRY(launch_after(packed_bwd_kernel<D, false>, dim3(kPackedCtas), Cq::kThreads, Cq::kSmem, st, 
+  PISA_TRY(launch_after(packed_bwd_kernel<D, false>, dim3(kPackedCtas), Cq::kThreads, Cq::kSmem, st,
       mq, mdo, mk, mv, p, scale, lse2, delta, s.out[0], s.head[0], s.row[0], nullptr, 0, 0, cuts[0], part[0]));
   // dk, dv: Q and dout one head at a time
   PISA_TRY(map_rows(&mq, q, true, D, p.T, p.Hq, 128));
   PISA_TRY(map_rows(&mdo, dout, true, D, p.T, p.Hq, 128));
   PISA_CUDA(cudaFuncSetAttribute(packed_bwd_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Ck::kSmem));
-  PISA_TRY(launch_after(packed_bwd_kernel<D, true>, dim3(kPackedCtas), Ck::kThreads, Ck::kSmem, st, 
+  PISA_TRY(launch_after(packed_bwd_kernel<D, true>, dim3(kPackedCtas), Ck::kThreads, Ck::kSmem, st,
       mq, mdo, mk, mv, p, scale, lse2, delta, s.out[1], s.head[1], s.row[1], s.out[2], s.head[2], s.row[2],
       cuts[1], part[1]));
   return launch_after(packed_sum_kernel<D>, dim3(kPackedCtas, D / 16, 3), 128, 0, st, s);

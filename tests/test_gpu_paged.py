@@ -68,6 +68,13 @@ CASES = [
     ([300], [555], 3, 3, 128, 256, BF),
     ([6, 40], [3, 10], 4, 4, 64, 16, BF),                # fewer keys than tokens: rows without any
     ([2, 3], [1, 0], 4, 4, 64, 16, BF),
+    ([8, 8], [200, 8], 12, 4, 64, 16, HF),               # drafts of one length: 24 rows in tiles of 30 of 32
+    ([6, 6, 6], [700, 20, 6], 10, 2, 128, 32, BF),       # 30 rows
+    ([32, 32], [45, 131], 3, 3, 128, 16, BF),            # 32 rows of one head
+    ([1, 1, 1], [400, 1, 333], 40, 2, 64, 64, BF),       # 20 rows, one token each
+    ([1] * 20 + [7], list(range(1, 21)) + [90], 4, 2, 128, 16, BF),   # single tokens and a few more: tiles of 16
+    ([0] * 9 + [8, 1], [5] * 9 + [260, 30], 24, 8, 64, 16, HF),       # as many tokens as requests, on two of them
+    ([1] * 20 + [70], [300] * 21, 20, 1, 128, 64, BF),   # a chunk among them: 128-row products
 ]
 
 
