@@ -29,11 +29,11 @@ template <int D, int R> struct RowsCfg {
   static constexpr int kTileBytes = kKeyTile * D * 2;       // K or V of a tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kQBytes = R * D * 2, kPBytes = R * kKeyTile * 2;
-  static constexpr int kFixed = kQBytes + kPBytes + 8 * R * 4 + 1024;
-  static constexpr int kMaxStages = (227 * 1024 - 1024 - kFixed) / kStageBytes;
+  static constexpr int kFixed = kPBytes + 8 * R * 4 + 1024;
+  static constexpr int kMaxStages = (227 * 1024 - 1024 - kFixed) / (kStageBytes + kQBytes);
   static constexpr int kStages = kMaxStages < 6 ? kMaxStages : 6;
-  static constexpr int kOffQ = kStages * kStageBytes;
-  static constexpr int kOffP = kOffQ + kQBytes;
+  static constexpr int kOffQ = kStages * kStageBytes;       // Q of a unit, with its first tile's stage
+  static constexpr int kOffP = kOffQ + kStages * kQBytes;
   static constexpr int kOffRed = kOffP + kPBytes;           // [8][R] f32
   static constexpr int kOffMisc = kOffRed + 8 * R * 4;      // barriers, schedule
   static constexpr int kSmem = kOffMisc + 1024 + 1024;      // + alignment slack
@@ -50,11 +50,13 @@ struct PagedKV {
 // that lie below kv.  All 32 lanes; lane i brings the i-th page, whose number
 // `page` it already holds.  A copy brings `rows` = min(page_size, 128) keys; a page
 // number outside the cache reads as zeros (the copy's own bounds check).
-// Returns the copies to make.
+
+// announces them, and `more` bytes on the same barrier; returns their number
 template <int D>
-__device__ __forceinline__ int expect_pages(uint32_t bar, int key0, int kv, int rows, int tensors, int lane) {
+__device__ __forceinline__ int expect_pages(uint32_t bar, int key0, int kv, int rows, int tensors, int more,
+                                            int lane) {
   const int live = kv - key0 <= 0 ? 0 : min((kv - key0 + rows - 1) / rows, kKeyTile / rows);
-  if (lane == 0) sm100::mbar_expect_tx(bar, (uint32_t)(live * rows * D * 2 * tensors));
+  if (lane == 0) sm100::mbar_expect_tx(bar, (uint32_t)(live * rows * D * 2 * tensors + more));
   __syncwarp();
   return live;
 }
@@ -62,7 +64,7 @@ __device__ __forceinline__ int expect_pages(uint32_t bar, int key0, int kv, int 
 template <int D>
 __device__ __forceinline__ void issue_pages_boxed(const CUtensorMap *m, uint32_t bar, uint32_t dst, int key0,
                                                   int kv, int head, int page, int rows, int page_size, int lane) {
-  if (lane < expect_pages<D>(bar, key0, kv, rows, 1, lane)) {
+  if (lane < expect_pages<D>(bar, key0, kv, rows, 1, 0, lane)) {
 #pragma unroll
     for (int b = 0; b < D / 64; ++b)
       sm100::tma_load_5d(dst + b * kKeyTile * 128 + lane * rows * 128, m, bar, 0, (key0 + lane * rows) % page_size, b,
@@ -76,8 +78,8 @@ __device__ __forceinline__ void issue_pages_boxed(const CUtensorMap *m, uint32_t
 template <int D>
 __device__ __forceinline__ void issue_pages_whole(const CUtensorMap *mk, const CUtensorMap *mv, uint32_t bar,
                                                   uint32_t dst, uint32_t v_off, int key0, int kv, int head,
-                                                  int page, int rows, int page_size, int lane) {
-  if (lane < expect_pages<D>(bar, key0, kv, rows, 2, lane)) {
+                                                  int page, int rows, int page_size, int more, int lane) {
+  if (lane < expect_pages<D>(bar, key0, kv, rows, 2, more, lane)) {
     const int row = (key0 + lane * rows) % page_size;
     const uint32_t d = dst + lane * rows * D * 2;
     sm100::tma_load_5d(d, mk, bar, 0, row, 0, head, page);
@@ -120,10 +122,9 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256
 
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
-    attend_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
+    attend_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PackedProblem p,
-                       const PagedKV cache, const T *q, long long q_head,
-                       long long q_row, float scale, const PackedOut o, PackedCut *__restrict__ cuts,
+                       const PagedKV cache, float scale, const PackedOut o, PackedCut *__restrict__ cuts,
                        float *__restrict__ part) {
   using C = RowsCfg<D, R>;
   using namespace sm100;
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
     *abort = 0;
   }
   if (tid == 32) {
+    prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
@@ -180,8 +182,17 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
           ok = false;
           break;
         }
+        const bool first = t == s.ta;   // Q comes with it
         issue_pages_whole<D>(&tm_k, &tm_v, full(st), sbase + st * C::kStageBytes, C::kTileBytes,
-                             t * kKeyTile, s.r.kv, s.h, page, page_rows, cache.page_size, lane);
+                             t * kKeyTile, s.r.kv, s.h, page, page_rows, cache.page_size,
+                             first ? p.tq * p.G * D * 2 : 0, lane);
+        if (first && elect_one()) {
+#pragma unroll
+          for (int b = 0; b < D / 64; ++b)
+            tma_load_4d(sbase + C::kOffQ + st * C::kQBytes + b * R * 128, &tm_q, full(st), 64 * b, 0,
+                        s.r.first + s.rt * p.tq, s.h);
+        }
+        __syncwarp();
         page = t + 1 < s.tb
                    ? lane_page(cache, s.b, (t + 1) * kKeyTile, s.r.kv, page_rows, lane)
                    : -1;
@@ -200,16 +211,9 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
   while (w.next(p)) {
     const PackedSegment s = w.s;
     const int tok0 = s.rt * p.tq, rows = min(s.r.n - tok0, p.tq) * p.G;
-    // Q of the unit: rows past the tile's are zero
-    consumers_sync();
-    for (int e = tid; e < R * (D / 8); e += C::kConsumers) {
-      const int row = e / (D / 8), ch = e % (D / 8);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (row < rows)
-        v = __ldcg(reinterpret_cast<const uint4 *>(q + (long long)(s.h * p.G + row % p.G) * q_head +
-                                                   (long long)(s.r.first + tok0 + row / p.G) * q_row + 8 * ch));
-      *reinterpret_cast<uint4 *>(smem + C::kOffQ + SwizzledTile<D>::offset(row, 8 * ch)) = v;
-    }
+    // Q of the unit as product operands, read once (rows past the tile's hold anything: their
+    // scores are masked, and a product's rows do not mix)
+    uint32_t qa[RT][D / 16][4];
     // keys each of this thread's rows sees: positions below lim
     int lim[RT][2];
 #pragma unroll
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) acc[i][n][x] = 0.f;
     }
-    consumers_sync();
+    consumers_sync();   // every warp has read the last unit's sums from `red`
     for (int t = s.ta; t < s.tb; ++t, ++it) {
       const int st = it % C::kStages;
       // a warp that gives up goes on through the same barriers, so that no other waits for it;
@@ -240,6 +244,17 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
           !__all_sync(0xffffffffu, mbar_wait(full(st), (it / C::kStages) & 1)))
         *abort = 1;
       const uint32_t ks = sbase + st * C::kStageBytes, vs = ks + C::kTileBytes;
+      if (t == s.ta) {
+        const uint32_t qs = sbase + C::kOffQ + st * C::kQBytes;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int row = 16 * i + (lane & 15), c = 2 * k + (lane >> 4);
+            ldmatrix_x4(qs + (c >> 3) * R * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4), qa[i][k][0], qa[i][k][1],
+                        qa[i][k][2], qa[i][k][3]);
+          }
+      }
       const int key0 = t * kKeyTile;
       const int live = s.r.kv - key0;    // keys of the tile that exist
       if (live < kKeyTile) {
@@ -267,12 +282,8 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
         ldmatrix_x4(ks + page_chunk<D>(krow, kc, lg), b[0], b[1], b[2], b[3]);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-          uint32_t a[4];
-          ldmatrix_x4(sbase + C::kOffQ +
-                          SwizzledTile<D>::offset(16 * i + (lane & 15), 16 * k + (lane >> 4) * 8),
-                      a[0], a[1], a[2], a[3]);
-          mma_16816<T>(sc[i][0], a, b[0], b[1]);
-          mma_16816<T>(sc[i][1], a, b[2], b[3]);
+          mma_16816<T>(sc[i][0], qa[i][k], b[0], b[1]);
+          mma_16816<T>(sc[i][1], qa[i][k], b[2], b[3]);
         }
       }
       // scores in units of log2; the row maximum of these 16 keys

@@ -72,18 +72,20 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
                                cudaStream_t st) {
   using C = RowsCfg<D, R>;
   p.tq = R / p.G;
-  // (at 1 / 1.5 / 2 tiles a unit: 158 / 152 / 149 us on 48 requests of 1 to 8000 keys, 957 MB; where
-  // units are short a larger count leaves CTAs idle)
-  p.unit_cost = 3 * kKeyTile / 2;
+  // (at 1.5 / 2 / 3 / 5 tiles a unit: 167 / 162 / 168 / 178 us on 300 requests of 1 to 1500 keys, 72 / 66 /
+  // 68 / 71 us on 300 of 1 to 300, 154 / 152 / 154 / 154 us on 48 of 1 to 8000)
+  p.unit_cost = 2 * kKeyTile;
   p.min_range = kKeyTile;
   p.whole = 0;
+  CUtensorMap mq;
+  PISA_TRY(map_query(&mq, q, Half16<T>::kBf16, D, p.G, p.T, p.Hkv, p.tq));
   const PackedScratch s = packed_scratch(D, R);
   PackedCut *cuts = (PackedCut *)(ws + s.cuts);
   float *part = (float *)(ws + s.part);
   PISA_CUDA(cudaFuncSetAttribute(attend_rows_kernel<T, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem));
   PISA_TRY(launch_after(attend_rows_kernel<T, D, R>, dim3(kPackedCtas), C::kThreads, C::kSmem, st,
-      mk, mv, p, cache, (const T *)q.data, q.head_stride, q.row_stride, scale, o, cuts, part));
+      mq, mk, mv, p, cache, scale, o, cuts, part));
   return launch_combine<T, D>(p, cuts, part, R, o, 0, st);
 }
 
