@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
   using namespace sm100;
   constexpr int RT = R / 16;            // m16 tiles
   constexpr int NT = D / 64;            // n8 tiles of a warp's output columns
+  constexpr int kStep = NT == 2 ? 1 : 2;   // 16 keys a step of P V
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -258,9 +259,10 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
       const int key0 = t * kKeyTile;
       const int live = s.r.kv - key0;    // keys of the tile that exist
       if (live < kKeyTile) {
-        // the rest of V may hold anything: zero, so that 0 x Inf or NaN never reaches a sum
-        const int z0 = max(live, 0);
-        for (int e = tid; e < (kKeyTile - z0) * (D / 8); e += C::kConsumers) {
+        // the rest of V may hold anything: zero, so that 0 x Inf or NaN never reaches a sum (up to
+        // the end of a step of the product: those behind are not read)
+        const int z0 = max(live, 0), z1 = (z0 + 16 * kStep - 1) & ~(16 * kStep - 1);
+        for (int e = tid; e < (z1 - z0) * (D / 8); e += C::kConsumers) {
           const int row = z0 + e / (D / 8), ch = e % (D / 8);
           *reinterpret_cast<uint4 *>(smem + st * C::kStageBytes + C::kTileBytes + page_chunk<D>(row, ch, lg)) =
               make_uint4(0u, 0u, 0u, 0u);
@@ -275,6 +277,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int x = 0; x < 4; ++x) sc[i][n][x] = 0.f;
+      if (16 * warp < live)
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         uint32_t b[4];
@@ -337,9 +340,8 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
           }
         }
       consumers_sync();
-      // O += P V for this warp's D / 8 columns
-#pragma unroll
-      for (int k = 0; k < kKeyTile / 16; k += (NT == 2 ? 1 : 2)) {
+      // O += P V for this warp's D / 8 columns, 16 kStep keys at a time
+      auto add = [&](int k) {
         uint32_t b[4];
         if (NT == 2) {
           const int vrow = 16 * k + (lane & 15), vc = 2 * warp + (lane >> 4);
@@ -364,6 +366,13 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
             mma_16816<T>(acc[i][0], a, b[2], b[3]);
           }
         }
+      };
+      if (live >= kKeyTile) {
+#pragma unroll
+        for (int k = 0; k < kKeyTile / 16; k += kStep) add(k);
+      } else {
+#pragma unroll 1
+        for (int k = 0; 16 * k < live; k += kStep) add(k);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(st));
