@@ -76,7 +76,6 @@ __global__ void __launch_bounds__(256)
 
 template <int D, bool KV> struct PackedBwdCfg {
   static constexpr int kThreads = 352;
-  static constexpr int kRows = 128;
   static constexpr int kStages = D == 128 ? (KV ? 4 : 6) : (KV ? 8 : 12);
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kBoxBytes = 128 * 128;

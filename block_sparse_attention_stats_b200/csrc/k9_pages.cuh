@@ -11,7 +11,8 @@
 // instead of a second launch or a wait between CTAs: at 1500 requests that is
 // 6 KB of lengths from L2 and one CTA-wide scan.  A row finds its request by
 // binary search; a slot on a fresh page comes from the free list, not from the
-// table, so no CTA waits for another's table entries.
+// table, so no CTA waits for another's table entries.  Replayed from a graph it
+// takes 3.8 us for 7 requests of up to 40 new tokens and 7.7 us for 1500 of up to 90.
 #pragma once
 
 #include "packed_primitives.cuh"
@@ -148,7 +149,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlan 
 // Write.  Row t of k and v goes to row slots[t] % ps of page slots[t] / ps, head
 // by head; rows whose slot is negative are left out.
 // Bound: HBM (each byte read once and written once).  One thread moves 16 bytes
-// of kRows rows, so that kRows loads are in flight before the first store.
+// of kWriteRows rows, so that that many loads are in flight before the first store.
+// 65000 rows of 8 heads, d = 128 (532 MB): 84 us, 6.3 TB/s, 0.97 of a plain copy's
+// rate.  33 rows: 1.8 us, the launch.
 struct PageWrite {
   const unsigned char *src[2];          // k, v
   long long src_head[2], src_row[2];    // strides in bytes

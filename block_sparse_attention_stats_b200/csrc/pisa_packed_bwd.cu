@@ -64,6 +64,9 @@ static pisa_status launch_packed_bwd(PackedProblem p, const pisa_rows &q, const 
       (const __nv_bfloat16 *)dout.data, dout.head_stride, dout.row_stride, out_f32, lse, p.Hq, p.T, p.cu, p.B,
       lse2, delta));
   p.tq = 128 / p.G;
+  // a unit's start and end in tiles, measured at 1.5 / 2.5 / 4: 2383 / 2228 / 2230 us a training step on 8192 +
+  // 4608 + 1500 tokens, 322 / 301 / 306 us on 4096 + 2048 at d = 64.  The shortest range at 1 / 3 / 6 tiles: 60 /
+  // 56 / 62 us on 512 + 100 tokens, where most units are cut
   p.unit_cost = 5 * kKeyTile / 2;
   p.min_range = 3 * kKeyTile;
   p.whole = 4 * kKeyTile;
