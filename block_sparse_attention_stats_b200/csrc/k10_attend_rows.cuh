@@ -68,15 +68,19 @@ __device__ __forceinline__ int expect_pages(uint32_t bar, int key0, int kv, int 
   __syncwarp();
   return live;
 }
-// 64-column boxes of all 128 keys one after the other, as tcgen05 reads them
+// K or V: 64-column boxes of all 128 keys one after the other, as tcgen05 reads them,
+// or (`whole`) page by page
 template <int D>
-__device__ __forceinline__ void issue_pages_boxed(const CUtensorMap *m, uint32_t bar, uint32_t dst, int key0,
-                                                  int kv, int head, int page, int rows, int page_size, int lane) {
+__device__ __forceinline__ void issue_pages(const CUtensorMap *m, uint32_t bar, uint32_t dst, int key0, int kv,
+                                            int head, int page, int rows, int page_size, bool whole, int lane) {
   if (lane < expect_pages<D>(bar, key0, kv, rows, 1, 0, lane)) {
+    const int row = (key0 + lane * rows) % page_size;
+    if (whole)
+      sm100::tma_load_5d(dst + lane * rows * D * 2, m, bar, 0, row, 0, head, page);
+    else
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b)
-      sm100::tma_load_5d(dst + b * kKeyTile * 128 + lane * rows * 128, m, bar, 0, (key0 + lane * rows) % page_size, b,
-                         head, page);
+      for (int b = 0; b < D / 64; ++b)
+        sm100::tma_load_5d(dst + b * kKeyTile * 128 + lane * rows * 128, m, bar, 0, row, b, head, page);
   }
   __syncwarp();
 }

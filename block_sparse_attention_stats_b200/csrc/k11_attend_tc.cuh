@@ -27,6 +27,12 @@
 // 8 heads, causal), 125 / 110 / 100 us on 16 x 1000 (16 / 16 heads).
 // S_ih of the next tile is issued after P_ih V_h of this one by the same thread, and one
 // thread's products run in order, so no barrier guards the overwrite.
+// Pages of 16 (D = 128): a page comes in one copy of 4 KB, its two 64-column boxes one
+// after the other, instead of two of 2 KB (32 copies a tile took as long as its products).
+// Groups of 8 keys are then 4 KB apart only if a half takes the same 8 rows of every
+// page: half h is the keys 16 g + 8 h + (0 .. 7), g = 0 .. 7, of the tile.  The order of
+// keys is free, and S, P and V follow the same one.  185 against 220 us on 2048 tokens
+// after 6952, 24 / 8 heads; pages of 64 take 180.
 // The running maximum moves only when it grows by more than 2^8 (weights stay
 // below 2^8, in range of both 16-bit types); a softmax thread then waits for the
 // product before, and rescales O_i itself.
@@ -62,22 +68,30 @@ template <int D> struct AttendCfg {
   static constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 };
 
+// Where the keys are: rows of a packed tensor, pages whose boxes are copied one by one, or
+// pages of 16 copied whole, with the halves of a tile spread over them (D = 128)
+enum KeySource { kPackedKeys, kPages, kSpreadPages };
+
 // tq1 tokens of a subtile; rows of subtile i, and its halves of key tiles
 struct SubTile {
   int rows, nh;
 };
-__device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedSegment &s, int tq1, int i) {
+__device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedSegment &s, int tq1, int i,
+                                           bool spread) {
   SubTile x;
   const int tok = s.rt * p.tq + i * tq1;
   x.rows = max(min(s.r.n - tok, tq1), 0) * p.G;
-  x.nh = x.rows == 0 ? 0 : (RowCost::length(p, s.r.n, s.r.kv, tq1, 2 * s.rt + i) + 63) / 64;
+  const int len = x.rows == 0 ? 0 : RowCost::length(p, s.r.n, s.r.kv, tq1, 2 * s.rt + i);
+  // (spread: the second half of the last tile begins with its key 8)
+  const int nt = packed_tiles(len);
+  x.nh = spread ? 2 * nt - (nt > 0 && len - (nt - 1) * kKeyTile <= 8) : (len + 63) / 64;
   return x;
 }
 
 // One row's part of 64 keys: scores from TMEM, running maximum and sum, weights
 // back as 16 bits over the scores' first 32 columns, O rescaled where the maximum
 // has moved (once `pv_done` says that the product before is in it).  `seen` columns
-// are visible.
+// are visible; SPREAD: those whose key, 16 (c / 8) + c % 8, is below `seen`.
 // A quarter of the exponentials as a polynomial on the multiply-add units did not
 // pay (918 against 893 us on 12000 + 700 + 4608 causal tokens).
 // The sum is of the float32 weights.  ROUNDED (where the float32 output is wanted
@@ -85,7 +99,7 @@ __device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedS
 // dout_t . o_t is then the mean of dP under the weights themselves, and does not lose
 // dP - Delta to their rounding where one key holds nearly all the weight; lse still
 // comes from the float32 weights, summed beside.
-template <typename T, int D, bool ROUNDED, typename Wait>
+template <typename T, int D, bool ROUNDED, bool SPREAD, typename Wait>
 __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, float sl2, int seen, Wait pv_done,
                                              float &m_run, float &l_run, float &e_run) {
   using namespace sm100;
@@ -94,12 +108,19 @@ __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, f
   tmem_ld_x32(s_addr + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
   tmem_wait_ld();
   auto sv = [&](int c) -> float { return __uint_as_float(r[c]); };
-  if (__any_sync(0xffffffffu, seen < 64)) {
+  if (__any_sync(0xffffffffu, seen < (SPREAD ? 120 : 64))) {
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       // bit c: column 32 w + c is visible
-      const int n = seen - 32 * w;
-      const uint32_t m = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+      uint32_t m;
+      if (SPREAD) {
+        m = 0u;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) m |= ((1u << min(max(seen - 64 * w - 16 * g, 0), 8)) - 1u) << (8 * g);
+      } else {
+        const int n = seen - 32 * w;
+        m = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+      }
 #pragma unroll
       for (int c = 0; c < 32; ++c) r[32 * w + c] = (m >> c) & 1u ? r[32 * w + c] : 0xff800000u;
     }
@@ -158,7 +179,7 @@ __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, f
   return true;
 }
 
-template <typename T, int D, bool PAGED, bool ROUNDED>
+template <typename T, int D, KeySource KEYS, bool ROUNDED>
 __global__ void __launch_bounds__(352, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const PackedProblem p,
@@ -178,6 +199,8 @@ __global__ void __launch_bounds__(352, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int tq1 = p.tq / 2, sub_rows = tq1 * p.G;
+  constexpr bool PAGED = KEYS != kPackedKeys, spread = KEYS == kSpreadPages;
+  static_assert(!spread || D == 128, "one box a page otherwise");
 
   if (warp == 1) {
     tmem_alloc(sbase + C::kOffMisc + 464, C::kTmemCols);
@@ -265,8 +288,8 @@ __global__ void __launch_bounds__(352, 1)
           }
           const uint32_t dst = sbase + C::kOffKV + st * C::kTileBytes;
           if constexpr (PAGED) {
-            issue_pages_boxed<D>(x ? &tm_v : &tm_k, bar(C::kBarFull + st), dst, t * kKeyTile, s.r.kv, s.h, page,
-                                 page_rows, cache.page_size, lane);
+            issue_pages<D>(x ? &tm_v : &tm_k, bar(C::kBarFull + st), dst, t * kKeyTile, s.r.kv, s.h, page, page_rows,
+                           cache.page_size, spread, lane);
           } else {
             if (elect_one()) {
               mbar_expect_tx(bar(C::kBarFull + st), C::kTileBytes);
@@ -306,12 +329,15 @@ __global__ void __launch_bounds__(352, 1)
     // S_ih of the tile whose K is in ring slot `ks`
     auto issue_s = [&](int h, int ks) {
       const uint64_t qd = smem_desc_sw128(sbase + C::kOffQ + i * C::kTileBytes, 16, 1024);
-      const uint64_t kd =
-          smem_desc_sw128(sbase + C::kOffKV + (ks % C::kStages) * C::kTileBytes + h * 64 * 128, 16, 1024);
+      const uint64_t kd = smem_desc_sw128(
+          sbase + C::kOffKV + (ks % C::kStages) * C::kTileBytes + h * (spread ? 1024 : 64 * 128), 16,
+          spread ? 4096 : 1024);
+      const uint64_t kbox = (spread ? 2048 : C::kBoxBytes) >> 4;
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + C::kColS + 128 * i + 64 * h, qd + step(k), kd + step(k), kIdS, k > 0 ? 1u : 0u);
+          mma_ss(tmem + C::kColS + 128 * i + 64 * h, qd + step(k), kd + (k >> 2) * kbox + (k & 3) * 2, kIdS,
+                 k > 0 ? 1u : 0u);
         tc_commit(bar(C::kBarS + 2 * h + i));
       }
       __syncwarp();
@@ -330,7 +356,7 @@ __global__ void __launch_bounds__(352, 1)
       x.ta = w.s.ta;
       x.tb = w.s.tb;
       x.kv = w.s.r.kv;
-      x.nh = min(subtile(p, w.s, tq1, i).nh, 2 * x.tb);
+      x.nh = min(subtile(p, w.s, tq1, i, spread).nh, 2 * x.tb);
       return true;
     };
     // S of a segment's first tile
@@ -381,8 +407,10 @@ __global__ void __launch_bounds__(352, 1)
               unsigned char *v = smem + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes;
               for (int e = lane; e < (kKeyTile - z0) * (D / 8); e += 32) {
                 const int row = z0 + e / (D / 8), ch = e % (D / 8);
-                *reinterpret_cast<uint4 *>(v + (ch >> 3) * C::kBoxBytes + row * 128 +
-                                           (((ch & 7) ^ (row & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4 *>(v + (spread ? page_chunk<D>(row, ch, 4)
+                                                       : (ch >> 3) * C::kBoxBytes + row * 128 +
+                                                             (((ch & 7) ^ (row & 7)) << 4))) =
+                    make_uint4(0u, 0u, 0u, 0u);
               }
               fence_proxy_async();
               __syncwarp();
@@ -399,12 +427,14 @@ __global__ void __launch_bounds__(352, 1)
           }
           tc_fence_after();
           const uint64_t vd = smem_desc_sw128(
-              sbase + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes, C::kBoxBytes, 1024);
+              sbase + C::kOffKV + ((slot + 1) % C::kStages) * C::kTileBytes + h * (spread ? 1024 : 4 * 2048),
+              spread ? 2048 : C::kBoxBytes, spread ? 4096 : 1024);
+          const uint64_t vstep = (spread ? 8192 : 2048) >> 4;
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ts(tmem + C::kColO + D * i, tmem + C::kColS + 128 * i + 64 * h + 8 * k,
-                     vd + (uint64_t)(((4 * h + k) * 2048) >> 4), kIdO, (!first || k > 0) ? 1u : 0u);
+                     vd + k * vstep, kIdO, (!first || k > 0) ? 1u : 0u);
             tc_commit(bar(C::kBarPV + i));
             if (2 * t + h + 1 == cur.nh) tc_commit(bar(C::kBarO + i));
           }
@@ -469,7 +499,7 @@ __global__ void __launch_bounds__(352, 1)
     bool ok = true;
     while (ok && w.next(p)) {
       const PackedSegment s = w.s;
-      const SubTile x = subtile(p, s, tq1, i);
+      const SubTile x = subtile(p, s, tq1, i, spread);
       const int tok = s.rt * p.tq + i * tq1 + row / p.G;     // token of this row in its sequence
       // keys this row sees: positions below lim (rows past the tile's go along with the last one)
       const int ltok = min(tok, s.r.n - 1);
@@ -487,8 +517,8 @@ __global__ void __launch_bounds__(352, 1)
         tc_fence_after();
         // the product of the half before: the one before that came before this S
         auto pv_done = [&]() { return uwait(bar(C::kBarPV + i), (nv - 1) & 1); };
-        if (!softmax_half<T, D, ROUNDED>(s_addr + 64 * h, o_addr, sl2, lim - u * 64, pv_done, m_run, l_run,
-                                         e_run)) {
+        const int seen = lim - (spread ? (u >> 1) * kKeyTile + 8 * h : u * 64);
+        if (!softmax_half<T, D, ROUNDED, spread>(s_addr + 64 * h, o_addr, sl2, seen, pv_done, m_run, l_run, e_run)) {
           ok = false;
           break;
         }

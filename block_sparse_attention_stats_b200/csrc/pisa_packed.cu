@@ -40,7 +40,7 @@ static pisa_status launch_combine(const PackedProblem &p, const PackedCut *cuts,
   return launch_after(packed_combine_kernel<T, D>, dim3(kPackedCtas, y), 128, 0, st, p, cuts, part, R, o, clear);
 }
 
-template <typename T, int D, bool PAGED, bool ROUNDED>
+template <typename T, int D, KeySource KEYS, bool ROUNDED>
 static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_rows &q, const CUtensorMap &mk,
                              const CUtensorMap &mv, float scale, const PackedOut &o, int clear,
                              unsigned char *ws, cudaStream_t st) {
@@ -59,9 +59,9 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
   const PackedScratch s = packed_scratch(D, C::kRows);
   PackedCut *cuts = (PackedCut *)(ws + s.cuts);
   float *part = (float *)(ws + s.part);
-  PISA_CUDA(cudaFuncSetAttribute(attend_tc_kernel<T, D, PAGED, ROUNDED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  PISA_CUDA(cudaFuncSetAttribute(attend_tc_kernel<T, D, KEYS, ROUNDED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  C::kSmem));
-  PISA_TRY(launch_after(attend_tc_kernel<T, D, PAGED, ROUNDED>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, mq, mk,
+  PISA_TRY(launch_after(attend_tc_kernel<T, D, KEYS, ROUNDED>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, mq, mk,
                         mv, p, cache, scale, o, cuts, part));
   return launch_combine<T, D>(p, cuts, part, C::kRows, o, clear, st);
 }
@@ -96,31 +96,37 @@ static pisa_status run_varlen(const PackedProblem &p, const pisa_rows &q, const 
   CUtensorMap mk, mv;
   PISA_TRY(map_rows(&mk, k, Half16<T>::kBf16, D, p.T, p.Hkv, kKeyTile));
   PISA_TRY(map_rows(&mv, v, Half16<T>::kBf16, D, p.T, p.Hkv, kKeyTile));
-  if (o.f32) return launch_tc<T, D, false, true>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
-  return launch_tc<T, D, false, false>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
+  if (o.f32) return launch_tc<T, D, kPackedKeys, true>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
+  return launch_tc<T, D, kPackedKeys, false>(p, PagedKV{}, q, mk, mv, scale, o, clear, ws, st);
 }
 
 template <typename T, int D>
 static pisa_status run_paged(const PackedProblem &p, const PagedKV &cache, const pisa_rows &q,
                              const pisa_pages &k, const pisa_pages &v, float scale, const PackedOut &o,
                              unsigned char *ws, cudaStream_t st) {
-  // Requests of up to 32 rows (tokens times the heads of a group) are for the kernel of few rows: 16
-  // requests of 8 tokens, 3 heads to a key head and 4000 keys take 61 / 62 us there and 73 / 59 with
-  // 128-row products (pages of 16 / 64), 48 of 5 tokens 138 / 127 and 188 / 141; requests of 33 to 64
-  // rows 97 - 101 and 79 - 80.  A longer one reads its keys once for every 32 rows there: 330 single
-  // tokens beside a chunk of 2900 took 3236 us, and 600 with 128-row products.
+  // Requests of up to 32 rows (tokens times the heads of a group) are for the kernel of few rows: 48
+  // requests of 5 tokens, 3 heads to a key head and 4000 keys take 137 / 127 us there (pages of 16 / 64)
+  // and 157 / 143 with 128-row products; 16 of 8 tokens (24 rows) 59 / 60 and 62 / 57; requests of 33 to
+  // 64 rows 97 - 101 and 79 - 80.  A longer one reads its keys once for every 32 rows there: 330 single
+  // tokens beside a chunk of 2900 took 3236 us, and 610 with 128-row products.
   // The lengths are on the device, and either kernel serves any of them.  So what T and B say
   // decides: T = k B is taken for k tokens a request, and other batches go to the kernel of few
   // rows where the tokens beyond one a request, were they all one request's, make a quarter as
-  // many tiles as there are requests (48 single tokens beside a chunk of 100: 143 against 188 us).
+  // many tiles as there are requests (48 single tokens beside a chunk of 100: 158 against 198 us).
   const long long r = std::max<long long>(((long long)p.T * p.G + p.B - 1) / p.B, p.G);
   const long long more = (long long)std::max(p.T - p.B, 0) * p.G;
   const bool few = r <= 32 && (p.T % p.B == 0 || more <= 8ll * p.B);
   CUtensorMap mk, mv;
-  const int halves = few ? D / 64 : 1;
+  const bool spread = D == 128 && cache.page_size == 16;
+  const int halves = few || spread ? D / 64 : 1;   // 64-column boxes in a copy
   PISA_TRY(map_pages(&mk, k, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages, halves));
   PISA_TRY(map_pages(&mv, v, Half16<T>::kBf16, D, cache.page_size, p.Hkv, cache.num_pages, halves));
-  if (!few) return launch_tc<T, D, true, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
+  if (!few) {
+    // (pages of 16 whole / box by box: 185 / 220 us on 2048 tokens after 6952, 24 / 8 heads)
+    if constexpr (D == 128)
+      if (spread) return launch_tc<T, D, kSpreadPages, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
+    return launch_tc<T, D, kPages, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
+  }
   if (r <= 16) return launch_rows<T, D, 16>(p, cache, q, mk, mv, scale, o, ws, st);
   return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
 }

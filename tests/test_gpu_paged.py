@@ -75,6 +75,11 @@ CASES = [
     ([1] * 20 + [7], list(range(1, 21)) + [90], 4, 2, 128, 16, BF),   # single tokens and a few more: tiles of 16
     ([0] * 9 + [8, 1], [5] * 9 + [260, 30], 24, 8, 64, 16, HF),       # as many tokens as requests, on two of them
     ([1] * 20 + [70], [300] * 21, 20, 1, 128, 64, BF),   # a chunk among them: 128-row products
+    # ends of tiles and of pages of 16 and 32, in 128-row products
+    ([40] * 12, [40, 41, 129, 136, 137, 144, 145, 247, 248, 249, 256, 257], 6, 2, 128, 16, BF),
+    ([23, 1, 8, 9, 130], [23, 1, 8, 9, 130], 12, 3, 128, 16, HF),
+    ([40] * 6, [40, 129, 159, 160, 161, 257], 6, 2, 128, 32, BF),
+    ([40, 200, 7], [20, 140, 3], 3, 3, 128, 16, BF),     # fewer keys than tokens
 ]
 
 
