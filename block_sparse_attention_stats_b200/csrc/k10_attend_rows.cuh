@@ -21,8 +21,8 @@
 // SMs load (2900); Q comes with a unit's first tile and stays in registers.
 // Measured (graph replays): 48 requests of 1 to 8000 keys, 40 / 8 heads, d = 128,
 // pages of 64 (957 MB) 151 us, 6.35 TB/s or 0.97 of a plain copy's rate; two requests of
-// 131072 and 90001 keys, 32 / 4 heads (453 MB) 80 us, of which the join of the parts and
-// the start are 9; one request of 777 keys, 8 heads, d = 64: 9.4 us, two launches; 300
+// 131072 and 90001 keys, 32 / 4 heads (453 MB) 78 us, of which the join of the parts and
+// the start are 7; one request of 777 keys, 8 heads, d = 64: 9.0 us, two launches; 300
 // requests of 1 to 300 keys (185 MB) 61 us, where a unit's start and end (a tile's time)
 // count as much as its tiles.
 #pragma once

@@ -363,12 +363,16 @@ __device__ __forceinline__ void clear_tail(const PackedProblem &p, int H, void *
 
 // Joins the partials of the unit that CTA blockIdx.x's range cuts:
 //   m = max_i m_i,  l = sum_i l_i 2^(m_i - m),  o = sum_i O_i 2^(m_i - m) / l
-// (m in units of log2).  One thread per (row, 16 columns): neighbouring threads
-// read neighbouring rows.
-template <typename T, int D>
+// (m in units of log2).  One thread per (row, 4 V columns): neighbouring threads
+// read neighbouring rows, and a thread's loads of 16 / V partials are in flight
+// together.  V = 4 where units have many rows; V = 2 where they have few, and a long
+// request tens of parts (V = 4 / 2 / 1: 80.0 / 78.0 / 78.4 us on 131072 and 90001 keys, 9.5 /
+// 9.0 / 9.3 us on one request of 777, 150 / 150 / 151 us on 48 of 1 to 8000).
+template <typename T, int D, int V>
 __global__ void __launch_bounds__(128)
     packed_combine_kernel(const PackedProblem p, const PackedCut *cuts,
                           const float *part, int R, const PackedOut o, int clear) {
+  constexpr int kBatch = 16 / V;
   sm100::wait_for_launches_before();
   if (clear)
     clear_tail<D>(p, p.Hq, o.out, o.head, o.row,
@@ -381,17 +385,17 @@ __global__ void __launch_bounds__(128)
   const int tok0 = cut.rt * p.tq, rows = min(r.n - tok0, p.tq) * p.G;
   const size_t slot = packed_slot_floats<D>(R);
   const int c0 = blockIdx.x, n = cut.last - c0 + 1;
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / 16); e += gridDim.y * blockDim.x) {
-    const int row = e % rows, c16 = e / rows;
-    float base = -INFINITY, l = 0.f, le = 0.f, acc[16];
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < rows * (D / (4 * V)); e += gridDim.y * blockDim.x) {
+    const int row = e % rows, c = e / rows;
+    float base = -INFINITY, l = 0.f, le = 0.f;
+    float4 acc[V];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-    // four partials at a time: their loads are in flight together
-    for (int i0 = 0; i0 < n; i0 += 4) {
-      float m[4], ls[4], es[4];
-      float4 x[4][4];
+    for (int j = 0; j < V; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float m[kBatch], ls[kBatch], es[kBatch];
+      float4 x[kBatch][V];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kBatch; ++k) {
         const int i = min(i0 + k, n - 1);
         // partial i: slot 1 of the first CTA, slot 0 of the later ones
         const float *s = part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot;
@@ -399,50 +403,47 @@ __global__ void __launch_bounds__(128)
         ls[k] = __ldcg(s + R + row);
         es[k] = __ldcg(s + 2 * R + row);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[k][j] = __ldcg(reinterpret_cast<const float4 *>(s + 3 * R) + (size_t)(4 * c16 + j) * R + row);
+        for (int j = 0; j < V; ++j)
+          x[k][j] = __ldcg(reinterpret_cast<const float4 *>(s + 3 * R) + (size_t)(V * c + j) * R + row);
         if (i0 + k >= n) m[k] = -INFINITY;
       }
-      const float top = fmaxf(fmaxf(base, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+      float top = base;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) top = fmaxf(top, m[k]);
       const float from = top == -INFINITY ? 0.f : top;
       const float f0 = exp2f(base - from);
       l *= f0;
       le *= f0;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) acc[j] *= f0;
+      for (int j = 0; j < V; ++j) acc[j] = make_float4(acc[j].x * f0, acc[j].y * f0, acc[j].z * f0, acc[j].w * f0);
       base = top;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kBatch; ++k) {
         const float f = exp2f(m[k] - from);
         if (f == 0.f) continue;   // no weight (and, of a tile without keys, no output either)
         l = fmaf(f, ls[k], l);
         le = fmaf(f, es[k], le);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[4 * j] = fmaf(f, x[k][j].x, acc[4 * j]);
-          acc[4 * j + 1] = fmaf(f, x[k][j].y, acc[4 * j + 1]);
-          acc[4 * j + 2] = fmaf(f, x[k][j].z, acc[4 * j + 2]);
-          acc[4 * j + 3] = fmaf(f, x[k][j].w, acc[4 * j + 3]);
-        }
+        for (int j = 0; j < V; ++j)
+          acc[j] = make_float4(fmaf(f, x[k][j].x, acc[j].x), fmaf(f, x[k][j].y, acc[j].y),
+                               fmaf(f, x[k][j].z, acc[j].z), fmaf(f, x[k][j].w, acc[j].w));
       }
     }
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;   // a row without keys is zero; NaN stays
-#pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] *= inv;
     const int token = r.first + tok0 + row / p.G, head = cut.h * p.G + row % p.G;
-    uint4 *dst = reinterpret_cast<uint4 *>(reinterpret_cast<T *>(o.out) + head * o.head + token * o.row + 16 * c16);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      dst[j] = make_uint4(Half16<T>::pack(acc[8 * j], acc[8 * j + 1]), Half16<T>::pack(acc[8 * j + 2], acc[8 * j + 3]),
-                          Half16<T>::pack(acc[8 * j + 4], acc[8 * j + 5]),
-                          Half16<T>::pack(acc[8 * j + 6], acc[8 * j + 7]));
     const size_t hr = (size_t)head * p.T + token;
-    if (o.f32)
+    T *dst = reinterpret_cast<T *>(o.out) + head * o.head + token * o.row + 4 * V * c;
+    uint2 w[V];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        reinterpret_cast<float4 *>(o.f32 + hr * D + 16 * c16)[j] =
-            make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-    if (o.lse && c16 == 0) o.lse[hr] = le == 0.f ? -INFINITY : (base + log2f(le)) * 0.6931471805599453f;
+    for (int j = 0; j < V; ++j) {
+      acc[j] = make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+      w[j] = make_uint2(Half16<T>::pack(acc[j].x, acc[j].y), Half16<T>::pack(acc[j].z, acc[j].w));
+      if (o.f32) reinterpret_cast<float4 *>(o.f32 + hr * D + 4 * V * c)[j] = acc[j];
+    }
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j)
+      reinterpret_cast<uint4 *>(dst)[j] = make_uint4(w[2 * j].x, w[2 * j].y, w[2 * j + 1].x, w[2 * j + 1].y);
+    if (o.lse && c == 0) o.lse[hr] = le == 0.f ? -INFINITY : (base + log2f(le)) * 0.6931471805599453f;
   }
 }
 

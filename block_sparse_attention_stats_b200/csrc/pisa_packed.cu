@@ -33,11 +33,11 @@ static PackedScratch packed_scratch(int d, int rows) {
 }
 
 // ---- launches ----------------------------------------------------------------------
-template <typename T, int D>
+template <typename T, int D, int V>
 static pisa_status launch_combine(const PackedProblem &p, const PackedCut *cuts, const float *part, int R,
                                   const PackedOut &o, int clear, cudaStream_t st) {
-  const int y = std::max(1, R * (D / 16) / 128);
-  return launch_after(packed_combine_kernel<T, D>, dim3(kPackedCtas, y), 128, 0, st, p, cuts, part, R, o, clear);
+  const int y = std::max(1, R * (D / (4 * V)) / 128);
+  return launch_after(packed_combine_kernel<T, D, V>, dim3(kPackedCtas, y), 128, 0, st, p, cuts, part, R, o, clear);
 }
 
 template <typename T, int D, KeySource KEYS, bool ROUNDED>
@@ -63,7 +63,7 @@ static pisa_status launch_tc(PackedProblem p, const PagedKV &cache, const pisa_r
                                  C::kSmem));
   PISA_TRY(launch_after(attend_tc_kernel<T, D, KEYS, ROUNDED>, dim3(kPackedCtas), C::kThreads, C::kSmem, st, mq, mk,
                         mv, p, cache, scale, o, cuts, part));
-  return launch_combine<T, D>(p, cuts, part, C::kRows, o, clear, st);
+  return launch_combine<T, D, 4>(p, cuts, part, C::kRows, o, clear, st);
 }
 
 template <typename T, int D, int R>
@@ -86,7 +86,7 @@ static pisa_status launch_rows(PackedProblem p, const PagedKV &cache, const pisa
                                  C::kSmem));
   PISA_TRY(launch_after(attend_rows_kernel<T, D, R>, dim3(kPackedCtas), C::kThreads, C::kSmem, st,
       mq, mk, mv, p, cache, scale, o, cuts, part));
-  return launch_combine<T, D>(p, cuts, part, R, o, 0, st);
+  return launch_combine<T, D, 2>(p, cuts, part, R, o, 0, st);
 }
 
 template <typename T, int D>

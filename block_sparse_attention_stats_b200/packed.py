@@ -235,7 +235,10 @@ def _laid_out(t):
 def varlen_attention(q, k, v, cu_seqlens, causal: bool = True,
                      scale: Optional[float] = None) -> torch.Tensor:
     """Attention over packed sequences, differentiable with respect to q, k and v (bf16; float16
-    without gradients).  Rows behind the last sequence are zero, and so are their gradients."""
+    without gradients).  Rows behind the last sequence are zero, and so are their gradients.
+    A training step can be captured into a CUDA graph; as with any autograd function, no eager
+    autograd graph of the same leaves may be alive then (autograd would make the capture wait for
+    the stream that graph was built on)."""
     q, k, v = (_laid_out(x) for x in (q, k, v))
     if torch.is_grad_enabled() and any(x.requires_grad for x in (q, k, v)):
         if q.dtype != torch.bfloat16:
@@ -279,8 +282,9 @@ def pisa_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens,
     status = L.load().pisa_paged_attention(
         _rows(q, q, "q"), _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"), _DT[q.dtype], pages, ps,
         _ints(block_table, (B, width), "block_table", q), width, _ints(cu_seqlens, (B + 1,), "cu_seqlens", q),
-        _ints(kv_lens, (B,), "kv_lens", q), B, T, Hq, Hkv, d, 0.0 if scale is None else float(scale), _rows(out, q, "out"),
-        _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size, _current_stream(q.get_device()))
+        _ints(kv_lens, (B,), "kv_lens", q), B, T, Hq, Hkv, d, 0.0 if scale is None else float(scale),
+        _rows(out, q, "out"), _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size,
+        _current_stream(q.get_device()))
     if status:
         _check("pisa_paged_attention", status)
     return out
@@ -368,8 +372,8 @@ def pisa_paged_step(q, k, v, k_cache, v_cache, past_lens, new_lens, block_table,
     status = L.load().pisa_paged_step(
         ctypes.byref(step), _rows(q, q, "q"), _rows(k, q, "k"), _rows(v, q, "v"),
         _pages(k_cache, q, "k_cache"), _pages(v_cache, q, "v_cache"), _DT[q.dtype], pages, Hq, Hkv, d,
-        0.0 if scale is None else float(scale), _rows(out, q, "out"), _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size,
-        _current_stream(q.get_device()))
+        0.0 if scale is None else float(scale), _rows(out, q, "out"),
+        _dense(lse, (Hq, T), torch.float32, "lse", q), ptr, size, _current_stream(q.get_device()))
     if status:
         _check("pisa_paged_step", status)
     return out, plan
