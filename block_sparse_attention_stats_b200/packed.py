@@ -229,6 +229,8 @@ class _VarlenAttention(torch.autograd.Function):
 
 def _laid_out(t):
     """t itself where the kernels can read it in place, else a contiguous copy."""
+    if t.is_contiguous() and not t.data_ptr() & 15 and not t.shape[-1] & 7:
+        return t
     return t if t.numel() == 0 or _strides_ok(t) else t.contiguous()
 
 
