@@ -295,22 +295,26 @@ def pisa_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens,
 def _page_step(past_lens, new_lens, block_table, free_pages, num_free, page_size, T, out):
     if block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("block_table must be [B, width], free_pages one-dimensional")
-    dev = block_table.device
-    B, width = block_table.shape
-    if out is None:
-        # the small results share one allocation
-        small = torch.empty(2 * B + 2, dtype=torch.int32, device=dev)
-        cu, kv, left = small.split((B + 1, B, 1))
-        out = dict(slots=torch.empty(T, dtype=torch.int64, device=dev), cu_seqlens=cu, kv_lens=kv, num_free=left)
     like = block_table
-    slots = out["slots"]
+    B, width = like.shape
+    if out is None:
+        dev = like.device
+        # the small results share one allocation
+        small, slots = (torch.empty(2 * B + 2, dtype=torch.int32, device=dev),
+                        torch.empty(T, dtype=torch.int64, device=dev))
+        cu, kv, left = small.split((B + 1, B, 1))
+        out = dict(slots=slots, cu_seqlens=cu, kv_lens=kv, num_free=left)
+        at = small.data_ptr()
+        results = slots.data_ptr(), at, at + 4 * (B + 1), at + 4 * (2 * B + 1)
+    else:
+        results = (_dense(out["slots"], (T,), torch.int64, "slots", like),
+                   _ints(out["cu_seqlens"], (B + 1,), "cu_seqlens", like),
+                   _ints(out["kv_lens"], (B,), "kv_lens", like), _ints(out["num_free"], (1,), "num_free", like))
     step = L.PisaPageStep(
         _ints(past_lens, (B,), "past_lens", like), _ints(new_lens, (B,), "new_lens", like), B, T,
-        _ints(block_table, (B, width), "block_table", like), width, page_size,
+        _ints(like, (B, width), "block_table", like), width, page_size,
         _ints(free_pages, free_pages.shape, "free_pages", like), free_pages.numel(),
-        _ints(num_free, (1,), "num_free", like), _dense(slots, (T,), torch.int64, "slots", like),
-        _ints(out["cu_seqlens"], (B + 1,), "cu_seqlens", like),
-        _ints(out["kv_lens"], (B,), "kv_lens", like), _ints(out["num_free"], (1,), "num_free", like))
+        _ints(num_free, (1,), "num_free", like), *results)
     return step, out
 
 
