@@ -135,8 +135,10 @@ __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, f
 #pragma unroll
   for (int c = 0; c < 8; ++c) mx[c] = fmaxf(mx[c], sv(c + 56));
   const float tmax = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-  const float m_t = tmax * sl2;
-  const bool grow = m_t > m_run + 8.0f;
+  // rounded up, and the growth taken as a difference: however large scores are, where their float32
+  // spacing is whole powers of two, no weight exceeds 2^8 (to nearest, weights became infinite there)
+  const float m_t = __fmul_ru(tmax, sl2);
+  const bool grow = m_t - m_run > 8.0f;
   const bool need_o = grow && m_run != -INFINITY;
   if (__any_sync(0xffffffffu, need_o)) {
     if (!pv_done()) return false;
