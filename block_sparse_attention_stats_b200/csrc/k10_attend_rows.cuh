@@ -218,6 +218,9 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
 
   // ======================= the eight working warps ============================
   const float sl2 = scale * kLog2e;
+  // weights are at most 1 here (the maximum is of all keys so far), so all of the type's room is theirs:
+  // f16 weights keep their precision down to 2^-29 of the largest, and vanish below 2^-40
+  constexpr float kLift = (float)Half16<T>::kRoom, kLower = 1.f / (float)(1 << Half16<T>::kRoom);
   const int g = lane >> 2, c2 = (lane & 3) * 2;
   int it = 0;
   while (w.next(p)) {
@@ -342,8 +345,12 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
           for (int n = 0; n < 2; ++n) {
             // P is rounded to 16 bits for the product (the tensor cores take no more); the sum
             // keeps the float32 weights, so only the weights' own rounding enters the output
-            const float p0 = ex2_approx(sc[i][n][2 * x] - base);
-            const float p1 = ex2_approx(sc[i][n][2 * x + 1] - base);
+            float z0 = sc[i][n][2 * x] - base, z1 = sc[i][n][2 * x + 1] - base;
+            if constexpr (Half16<T>::kRoom != 0) {
+              z0 += kLift;
+              z1 += kLift;
+            }
+            const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
             l[i][x] += p0 + p1;
             *reinterpret_cast<uint32_t *>(smem + C::kOffP +
                                           SwizzledTile<kKeyTile>::offset(row, 16 * warp + 8 * n + c2)) =
@@ -420,18 +427,19 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
                 Half16<T>::pack(acc[i][n][2 * x] * inv, acc[i][n][2 * x + 1] * inv);
           if (head_lane && o.lse)
             o.lse[(size_t)head * p.T + token] =
-                ls == 0.f ? -INFINITY : (m[i][x] + log2f(ls)) * 0.6931471805599453f;
+                ls == 0.f ? -INFINITY : (m[i][x] + log2f(ls * kLower)) * 0.6931471805599453f;
         } else {
+          // (a power of two: exact)
           if (head_lane) {
             slot[row] = m[i][x];
-            slot[R + row] = ls;
-            slot[2 * R + row] = ls;
+            slot[R + row] = ls * kLower;
+            slot[2 * R + row] = ls * kLower;
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const int col = warp * (D / 8) + 8 * n + c2;
             *reinterpret_cast<float2 *>(slot + 3 * R + ((size_t)(col >> 2) * R + row) * 4 + (col & 3)) =
-                make_float2(acc[i][n][2 * x], acc[i][n][2 * x + 1]);
+                make_float2(acc[i][n][2 * x] * kLower, acc[i][n][2 * x + 1] * kLower);
           }
         }
       }

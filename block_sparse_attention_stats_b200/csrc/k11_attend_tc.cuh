@@ -33,9 +33,14 @@
 // page: half h is the keys 16 g + 8 h + (0 .. 7), g = 0 .. 7, of the tile.  The order of
 // keys is free, and S, P and V follow the same one.  185 against 220 us on 2048 tokens
 // after 6952, 24 / 8 heads; pages of 64 take 180.
-// The running maximum moves only when it grows by more than 2^8 (weights stay
-// below 2^8, in range of both 16-bit types); a softmax thread then waits for the
-// product before, and rescales O_i itself.
+// The running maximum moves only when it grows by more than 2^8 (f16: 2^4); a softmax
+// thread then waits for the product before, and rescales O_i itself.  f16 weights are
+// formed 2^11 times as large (Half16, packed_schedule.cuh), so they stay below 2^15,
+// keep their precision down to 2^-25 of the largest and vanish below 2^-36.  (A growth of
+// 2^8 / 2^4 / 2^2 / 2 leaves a factor of 2^7 / 2^11 / 2^13 / 2^14 and takes 884 / 902 / 1006 / 1020
+// us on 12000 + 700 + 4608 f16 tokens, 24 / 8 heads; with 2^7 a tail of weights 2^-24 is off by
+// up to 2^-8.  Where queries are large and maxima move often it costs more: 315 / 349 us at 2^8 /
+// 2^4 on 8000 + 3000 tokens, 16 / 4 heads, scores of deviation 4.)
 // Every wait is bounded; on a timeout the CTA records the error, stops issuing,
 // drains its copies and products, frees TMEM and exits.
 #pragma once
@@ -135,10 +140,13 @@ __device__ __forceinline__ bool softmax_half(uint32_t s_addr, uint32_t o_addr, f
 #pragma unroll
   for (int c = 0; c < 8; ++c) mx[c] = fmaxf(mx[c], sv(c + 56));
   const float tmax = max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-  // rounded up, and the growth taken as a difference: however large scores are, where their float32
-  // spacing is whole powers of two, no weight exceeds 2^8 (to nearest, weights became infinite there)
-  const float m_t = __fmul_ru(tmax, sl2);
-  const bool grow = m_t - m_run > 8.0f;
+  // m_run is what is subtracted: the maximum, less the factor of f16 weights.  Both roundings go
+  // up, and the growth is a difference: however large scores are, where their float32 spacing is
+  // whole powers of two, no weight leaves the type's range (to nearest, weights became infinite there)
+  constexpr float kGrow = Half16<T>::kBf16 ? 8.f : 4.f;
+  float m_t = __fmul_ru(tmax, sl2);
+  if constexpr (!Half16<T>::kBf16) m_t = __fsub_ru(m_t, Half16<T>::kRoom - kGrow);
+  const bool grow = m_t - m_run > kGrow;
   const bool need_o = grow && m_run != -INFINITY;
   if (__any_sync(0xffffffffu, need_o)) {
     if (!pv_done()) return false;

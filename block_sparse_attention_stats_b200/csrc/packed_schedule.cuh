@@ -294,9 +294,15 @@ template <int D> __host__ __device__ constexpr size_t packed_slot_floats(int R) 
   return (size_t)R * (D + 3);
 }
 
+// A softmax weight is rounded to T for its product with the values.  bf16 has float32's range; f16's
+// spacing stops shrinking at 2^-14 and ends at 2^-24, so of a weight far below the largest little or
+// nothing would be left there, while the sum has all of it: of one key 2^17.4 above 131071 others,
+// whose values are 1, came 0.9964.  So f16 weights are formed larger by a power of two, where the
+// type still has room above (kRoom), and the factor, common to the weights and their sum, cancels.
 template <typename T> struct Half16;
 template <> struct Half16<__nv_bfloat16> {
   static constexpr bool kBf16 = true;
+  static constexpr int kRoom = 0;
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
   static __device__ __forceinline__ float2 unpack(uint32_t x) {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
@@ -304,6 +310,7 @@ template <> struct Half16<__nv_bfloat16> {
 };
 template <> struct Half16<__half> {
   static constexpr bool kBf16 = false;
+  static constexpr int kRoom = 15;   // the largest weight is 2^15 at most
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&v);

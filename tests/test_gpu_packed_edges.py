@@ -55,3 +55,76 @@ def test_scores_past_every_range(P, dtype):
                                    scale=scale)
         P.pisa_device_status()
         assert torch.isfinite(a.float()).all() and torch.isfinite(b.float()).all()
+
+
+# ---- f16 weights far below the largest ------------------------------------------------------------
+
+def sink(n, d, gap, spread):
+    """A query, n keys and values of one head: key 0 scores 2^gap times the weight of the others (which
+    vary by `spread`), and its value is zero, so the output is the tail's alone."""
+    q = torch.zeros(1, d)
+    q[0, 0] = 4
+    k = rows(1, n, d, dtype=torch.float32) * spread
+    k[:, 0] = k[:, 0] if spread else 0
+    k[0] = 0
+    k[0, 0] = 4
+    v = (0.5 + torch.rand(n, d, generator=torch.Generator().manual_seed(2))) if spread else \
+        (0.5 + torch.rand(1, d, generator=torch.Generator().manual_seed(2))).expand(n, d).clone()
+    v[0] = 0
+    return q.half(), k.half(), v.half(), gap * math.log(2) / 16
+
+
+GAPS = [(18.3, 0.0), (23.7, 0.0), (25.6, 0.0), (26.7, 0.0), (23.7, 0.05)]
+
+
+@pytest.mark.parametrize("gap,spread", GAPS)
+@pytest.mark.parametrize("new,hq,kv,d,ps", [(1, 2, [131072], 64, 64), (1, 1, [90001], 128, 16),
+                                            (5, 4, [20000], 64, 128), (1, 2, [3000] * 40, 64, 16),
+                                            (70, 2, [131072], 64, 64), (300, 1, [50001], 128, 16),
+                                            (40, 4, [3000] * 20, 128, 32)])
+def test_f16_tails_of_long_caches(P, new, hq, kv, d, ps, gap, spread):
+    """One key far above a long tail: the tail is in the output with its whole weight."""
+    m = kv[0]
+    q, k, v, scale = sink(m, d, gap, spread)
+    q = q.expand(new, d)
+    pages = -(-m // ps)
+    kc, vc = (pages_of(x[None], ps).cuda() for x in (k, v))
+    table = i32([list(range(pages))] * len(kv))                 # every request reads the same pages
+    T = new * len(kv)
+    qs = q.repeat(len(kv), 1)[None].expand(hq, T, d).contiguous().cuda()
+    lse = torch.zeros(hq, T, device="cuda")
+    out = P.pisa_paged_attention(qs, kc, vc, table, i32([new * b for b in range(len(kv) + 1)]), i32(kv), scale=scale,
+                                 lse=lse)
+    P.pisa_device_status()
+    _, want, bound, ln, ln_bound, _ = U.attend(q.double(), k.double(), v.double(), torch.arange(m - new, m), scale,
+                                               U.half_step(HF))
+    for b in range(len(kv)):
+        r = slice(b * new, (b + 1) * new)
+        for h in range(hq):
+            U.check(out[h, r], want, bound, f"request {b} head {h}")
+            U.check(lse[h, r], ln, ln_bound, f"lse of request {b} head {h}")
+
+
+@pytest.mark.parametrize("gap,spread", GAPS)
+@pytest.mark.parametrize("lens,d", [([20000], 64), ([9000, 300, 4000], 128)])
+def test_f16_tails_of_long_prompts(P, lens, d, gap, spread):
+    n = max(lens)
+    q, k, v, scale = sink(n, d, gap, spread)
+    T = sum(lens)
+    qs = q.expand(T, d)[None].contiguous().cuda()
+    ks, vs = (torch.cat([x[:m] for m in lens])[None].cuda() for x in (k, v))
+    cu = i32(U.offsets(lens))
+    for f32 in (None, torch.zeros(1, T, d, device="cuda")):
+        lse = torch.zeros(1, T, device="cuda")
+        out = P.pisa_varlen_attention(qs, ks, vs, cu, scale=scale, lse=lse, out_f32=f32)
+        P.pisa_device_status()
+        for a, m in zip(U.offsets(lens), lens):
+            at = torch.tensor(sorted({0, 1, 130, 299, m // 2, m - 2, m - 1}))
+            at = at[at < m]
+            _, want, bound, ln, ln_bound, _ = U.attend(q.expand(len(at), d).double(), k[:m].double(), v[:m].double(),
+                                                       at, scale, U.half_step(HF))
+            U.check(out[0, a + at], want, bound, f"out of {m}")
+            U.check(lse[0, a + at], ln, ln_bound, f"lse of {m}")
+            if f32 is not None:
+                U.check(f32[0, a + at].half(), want, bound, f"out_f32 of {m}")
+
