@@ -630,9 +630,9 @@ template <int D> __global__ void __launch_bounds__(128) packed_sum_kernel(const 
   __nv_bfloat16 *out = a.out[z];
   const long long hs = a.head[z], rs = a.row[z];
   if (a.clear)
-    clear_tail<D>(p, kv ? p.Hkv : p.Hq, out, hs, rs,
-                  ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
-                  (long long)gridDim.x * gridDim.y * blockDim.x);
+    clear_unused<D>(p, kv ? p.Hkv : p.Hq, out, hs, rs,
+                    ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                    (long long)gridDim.x * gridDim.y * blockDim.x);
   const PackedCut cut = packed_cut_at(a.cuts[kv], blockIdx.x);
   if (!cut.valid) return;
   bool bad = false;

@@ -353,16 +353,18 @@ struct PackedOut {
   float *f32;               // [Hq, T, D] or nullptr
 };
 
-// Zeros rows [cu[B], T) of a 16-bit tensor of H heads: rows that belong to no
+// Zeros rows [0, cu[0]) and [cu[B], T) of a 16-bit tensor of H heads: rows that belong to no
 // sequence.  All threads of a grid of `threads` threads, this one the `me`-th.
 template <int D>
-__device__ __forceinline__ void clear_tail(const PackedProblem &p, int H, void *out, long long head_stride,
-                                           long long row_stride, long long me, long long threads) {
-  const int end = min(max(sm100::ld_int(p.cu + p.B), 0), p.T);
-  const long long n = (long long)H * (p.T - end) * (D / 8);
+__device__ __forceinline__ void clear_unused(const PackedProblem &p, int H, void *out, long long head_stride,
+                                             long long row_stride, long long me, long long threads) {
+  const int first = min(max(sm100::ld_int(p.cu), 0), p.T);
+  const int end = max(min(sm100::ld_int(p.cu + p.B), p.T), first);
+  const int rows = first + p.T - end;
+  const long long n = (long long)H * rows * (D / 8);
   for (long long e = me; e < n; e += threads) {
     const long long r = e / (D / 8);
-    const int h = (int)(r / (p.T - end)), t = end + (int)(r % (p.T - end));
+    const int h = (int)(r / rows), i = (int)(r % rows), t = i < first ? i : end + i - first;
     reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + h * head_stride + t * row_stride)[e % (D / 8)] =
         make_uint4(0u, 0u, 0u, 0u);
   }
@@ -382,9 +384,9 @@ __global__ void __launch_bounds__(128)
   constexpr int kBatch = 16 / V;
   sm100::wait_for_launches_before();
   if (clear)
-    clear_tail<D>(p, p.Hq, o.out, o.head, o.row,
-                  ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
-                  (long long)gridDim.x * gridDim.y * blockDim.x);
+    clear_unused<D>(p, p.Hq, o.out, o.head, o.row,
+                    ((long long)blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x,
+                    (long long)gridDim.x * gridDim.y * blockDim.x);
   const PackedCut cut = packed_cut_at(cuts, blockIdx.x);
   if (!cut.valid) return;
   bool bad = false;

@@ -146,7 +146,8 @@ def pisa_varlen_attention(q, k, v, cu_seqlens, causal: bool = True, scale: Optio
     """Attention of every sequence of a packed batch over itself: q [Hq, T, d], k and v
     [Hkv, T, d] (bf16 or float16), cu_seqlens int32 [B + 1] on the device.  `lse` (float32
     [Hq, T]) and `out_f32` (float32 [Hq, T, d]) are written if given; the backward needs both.
-    Rows of `out` behind the last sequence keep what they held, or become zero with `zero_tail`."""
+    Rows of `out` that belong to no sequence (behind the last, before the first) keep what they held,
+    or become zero with `zero_tail`."""
     Hq, T, d, Hkv = _heads(q, k, v)
     away = _elsewhere(q, stream)
     if away is not None:
@@ -237,7 +238,7 @@ def _laid_out(t):
 def varlen_attention(q, k, v, cu_seqlens, causal: bool = True,
                      scale: Optional[float] = None) -> torch.Tensor:
     """Attention over packed sequences, differentiable with respect to q, k and v (bf16; float16
-    without gradients).  Rows behind the last sequence are zero, and so are their gradients.
+    without gradients).  Rows that belong to no sequence are zero, and so are their gradients.
     A training step can be captured into a CUDA graph; as with any autograd function, no eager
     autograd graph of the same leaves may be alive then (autograd would make the capture wait for
     the stream that graph was built on)."""

@@ -292,8 +292,8 @@ size_t pisa_dense_attention_workspace_bytes(int B, int H, int L, int d, pisa_dty
  *    aligned; the stride of an extent of one is not used.
  *  - Sequence b holds rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (device
  *    int32 [B + 1], ascending, within [0, T]); a sequence may be empty.  Rows
- *    behind the last sequence are neither read into any result nor written
- *    (unless PISA_ZERO_TAIL is set).
+ *    behind the last sequence, and before the first where cu_seqlens[0] > 0, are
+ *    neither read into any result nor written (unless PISA_ZERO_TAIL is set).
  *  - Query head h reads key head h / (Hq / Hkv); Hq is a multiple of Hkv, and
  *    Hq / Hkv at most 128.  d is 64 or 128.  B is at most 65536, T 2^24, a request
  *    at most 2^30 positions long.  dtype is PISA_BF16 or PISA_F16
@@ -327,8 +327,8 @@ typedef struct {
 
 /* flags of the varlen calls */
 #define PISA_CAUSAL 1    /* token i sees tokens 0 .. i; else all of its sequence */
-#define PISA_ZERO_TAIL 2 /* rows behind the last sequence are set to zero (out, dq, dk, dv;
-                            not lse and out_f32) instead of left as they were */
+#define PISA_ZERO_TAIL 2 /* rows behind the last sequence and before the first are set to zero
+                            (out, dq, dk, dv; not lse and out_f32) instead of left as they were */
 
 size_t pisa_varlen_attention_workspace_bytes(int Hq, int Hkv, int d);
 

@@ -128,3 +128,42 @@ def test_f16_tails_of_long_prompts(P, lens, d, gap, spread):
             if f32 is not None:
                 U.check(f32[0, a + at].half(), want, bound, f"out_f32 of {m}")
 
+
+
+# ---- rows of no sequence ---------------------------------------------------------------------------
+
+def stale(*like):
+    """Memory of the allocator that holds NaN: what an uninitialised result would show."""
+    held = [torch.full_like(x, math.nan) for x in like for _ in range(4)]
+    torch.cuda.synchronize()
+    del held
+
+
+@pytest.mark.parametrize("cu,T", [([5, 40, 100], 130), ([7, 7, 9], 9), ([130, 130], 130), ([3, 500], 500)])
+def test_rows_before_the_first_sequence_are_zero(P, cu, T):
+    hq, hkv, d = 4, 2, 64
+    q, k, v, g = (rows(i, h, T, d).cuda() for i, h in ((1, hq), (2, hkv), (3, hkv), (4, hq)))
+    a, b = cu[0], cu[-1]
+    stale(q, k, v)
+    plain = P.varlen_attention(q, k, v, i32(cu))
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    stale(q, k, v)
+    out = P.varlen_attention(*leaves, i32(cu))
+    stale(q, k, v)
+    grads = torch.autograd.grad(out, leaves, g)
+    P.pisa_device_status()
+    for x in (plain, out, *grads):
+        assert (x[:, :a] == 0).all() and (x[:, b:] == 0).all()
+    # the sequences themselves: as where they begin at row 0
+    if b > a:
+        cut = [x[:, a:b].detach().contiguous().requires_grad_() for x in (q, k, v)]
+        ref = P.varlen_attention(*cut, i32([c - a for c in cu]))
+        assert torch.equal(out[:, a:b], ref)
+        with torch.no_grad():
+            assert torch.equal(plain[:, a:b], P.varlen_attention(*cut, i32([c - a for c in cu])))
+        for x, y in zip(grads, torch.autograd.grad(ref, cut, g[:, a:b].contiguous())):
+            assert torch.equal(x[:, a:b], y)
+    # without zero_tail they keep what they held
+    kept = torch.full_like(q, 7.0)
+    P.pisa_varlen_attention(q, k, v, i32(cu), out=kept)
+    assert (kept[:, :a] == 7).all() and (kept[:, b:] == 7).all() and torch.equal(kept[:, a:b], plain[:, a:b])
