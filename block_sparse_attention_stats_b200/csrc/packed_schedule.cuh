@@ -414,7 +414,10 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
         for (int j = 0; j < V; ++j)
           x[k][j] = __ldcg(reinterpret_cast<const float4 *>(s + 3 * R) + (size_t)(V * c + j) * R + row);
-        if (i0 + k >= n) m[k] = -INFINITY;
+        if (i0 + k >= n) {
+          m[k] = -INFINITY;
+          ls[k] = 0.f;
+        }
       }
       float top = base;
 #pragma unroll
@@ -428,8 +431,10 @@ __global__ void __launch_bounds__(128)
       base = top;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
+        // no key seen (of a tile without keys the slot holds no output either).  A sum of NaN comes
+        // with no maximum too, where every score is NaN, and is not passed over
+        if (m[k] == -INFINITY && ls[k] == 0.f) continue;
         const float f = exp2f(m[k] - from);
-        if (f == 0.f) continue;   // no weight (and, of a tile without keys, no output either)
         l = fmaf(f, ls[k], l);
         le = fmaf(f, es[k], le);
 #pragma unroll

@@ -167,3 +167,53 @@ def test_rows_before_the_first_sequence_are_zero(P, cu, T):
     kept = torch.full_like(q, 7.0)
     P.pisa_varlen_attention(q, k, v, i32(cu), out=kept)
     assert (kept[:, :a] == 7).all() and (kept[:, b:] == 7).all() and torch.equal(kept[:, a:b], plain[:, a:b])
+
+
+# ---- non-finite queries -------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("new,kv,ps,d", [([1, 1], [50000, 300], 64, 128), ([40, 1], [50000, 300], 64, 128),
+                                         ([1, 1], [50, 30], 16, 64), ([40, 3], [50, 30], 16, 128)])
+def test_a_query_of_nan_gives_nan_and_touches_no_other_row(P, new, kv, ps, d):
+    """Also where the request's keys are shared out over many blocks, whose parts are joined."""
+    hq, hkv = 4, 2
+    need = [-(-m // ps) for m in kv]
+    kc, vc = (rows(i, sum(need), hkv, ps, d).cuda() for i in (2, 3))
+    table = torch.full((2, max(need)), -1)
+    table[0, :need[0]], table[1, :need[1]] = torch.arange(need[0]), torch.arange(need[0], sum(need))
+    q = rows(1, hq, sum(new), d).cuda()
+    dirty = q.clone()
+    bad = new[0] // 2
+    dirty[1, bad] = math.nan
+
+    def call(x):
+        lse = torch.zeros(hq, sum(new), device="cuda")
+        return P.pisa_paged_attention(x, kc, vc, i32(table.tolist()), i32(U.offsets(new)), i32(kv), lse=lse), lse
+
+    a, b = call(q), call(dirty)
+    P.pisa_device_status()
+    for x, y in zip(a, b):
+        assert torch.isnan(y[1, bad]).all()
+        keep = torch.ones(x.shape[:2], dtype=torch.bool)
+        keep[1, bad] = False
+        assert torch.equal(x[keep], y[keep])
+
+
+@pytest.mark.parametrize("lens,row", [([6000], 5990), ([300, 20], 311)])
+def test_a_query_of_nan_in_a_prompt(P, lens, row):
+    T, d = sum(lens), 64
+    q, k, v = (rows(i, h, T, d).cuda() for i, h in ((1, 2), (2, 1), (3, 1)))
+    dirty = q.clone()
+    dirty[0, row] = math.nan
+
+    def call(x, f32):
+        lse = torch.zeros(2, T, device="cuda")
+        return P.pisa_varlen_attention(x, k, v, i32(U.offsets(lens)), lse=lse, out_f32=f32), lse
+
+    for f32 in (None, torch.zeros(2, T, d, device="cuda")):
+        a, b = call(q, f32), call(dirty, f32)
+        P.pisa_device_status()
+        for x, y in zip(a, b):
+            assert torch.isnan(y[0, row]).all()
+            keep = torch.ones(x.shape[:2], dtype=torch.bool)
+            keep[0, row] = False
+            assert torch.equal(x[keep], y[keep])
