@@ -104,18 +104,20 @@ template <typename T, int D>
 static pisa_status run_paged(const PackedProblem &p, const PagedKV &cache, const pisa_rows &q,
                              const pisa_pages &k, const pisa_pages &v, float scale, const PackedOut &o,
                              unsigned char *ws, cudaStream_t st) {
-  // Requests of up to 32 rows (tokens times the heads of a group) are for the kernel of few rows: 48
-  // requests of 5 tokens, 3 heads to a key head and 4000 keys take 137 / 127 us there (pages of 16 / 64)
-  // and 157 / 143 with 128-row products; 16 of 8 tokens (24 rows) 59 / 60 and 62 / 57; requests of 33 to
-  // 64 rows 97 - 101 and 79 - 80.  A longer one reads its keys once for every 32 rows there: 330 single
-  // tokens beside a chunk of 2900 took 3236 us, and 610 with 128-row products.
-  // The lengths are on the device, and either kernel serves any of them.  So what T and B say
-  // decides: T = k B is taken for k tokens a request, and other batches go to the kernel of few
-  // rows where the tokens beyond one a request, were they all one request's, make a quarter as
-  // many tiles as there are requests (48 single tokens beside a chunk of 100: 158 against 198 us).
+  // Requests of up to 16 rows (tokens times the heads of a group) are for the kernel of few rows: single
+  // tokens of 3 to 16 heads a key head, or drafts of 2 to 5, take 0.76 to 0.88 of the time of 128-row
+  // products there (48 single tokens over 4000 keys: 127 against 145 us; 100 over 300: 15.6 and 20.6;
+  // 64 drafts of 4: 165 and 191).  Of more rows it gains nothing: a form with 32 took 0.95 to 1.07 of the
+  // time for single tokens of 17 to 32 heads and 1.06 to 1.23 for drafts.
+  // The lengths are on the device, and either kernel serves any of them, but this one reads a request's
+  // keys once for every 16 rows.  So it is taken only where what T allows beyond one token a request,
+  // were it all one request's, is 64 rows: beside 48 single tokens over 4000 keys, a chunk over 60000
+  // takes 1.05 / 1.11 / 1.18 / 1.5 / 2.1 / 3.1 times as long here at 24 / 64 / 64 / 96 / 192 / 384 rows, and
+  // 330 single tokens beside a chunk of 2980 took 3222 us here, 613 there.  T says no more than that: a batch
+  // of T = k B rows may be k tokens each, or one chunk and padding, so drafts of large batches forgo the
+  // seventh that they would gain (64 of 4: 191 us).
   const long long r = std::max<long long>(((long long)p.T * p.G + p.B - 1) / p.B, p.G);
-  const long long more = (long long)std::max(p.T - p.B, 0) * p.G;
-  const bool few = r <= 32 && (p.T % p.B == 0 || more <= 8ll * p.B);
+  const bool few = r <= 16 && (long long)std::max(p.T - p.B, 0) * p.G <= 64;
   CUtensorMap mk, mv;
   const bool spread = D == 128 && cache.page_size == 16;
   const int halves = few || spread ? D / 64 : 1;   // 64-column boxes in a copy
@@ -127,8 +129,7 @@ static pisa_status run_paged(const PackedProblem &p, const PagedKV &cache, const
       if (spread) return launch_tc<T, D, kSpreadPages, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
     return launch_tc<T, D, kPages, false>(p, cache, q, mk, mv, scale, o, 0, ws, st);
   }
-  if (r <= 16) return launch_rows<T, D, 16>(p, cache, q, mk, mv, scale, o, ws, st);
-  return launch_rows<T, D, 32>(p, cache, q, mk, mv, scale, o, ws, st);
+  return launch_rows<T, D, 16>(p, cache, q, mk, mv, scale, o, ws, st);
 }
 
 // ---- argument checks --------------------------------------------------------------------

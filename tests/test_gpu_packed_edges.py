@@ -217,3 +217,23 @@ def test_a_query_of_nan_in_a_prompt(P, lens, row):
             keep = torch.ones(x.shape[:2], dtype=torch.bool)
             keep[0, row] = False
             assert torch.equal(x[keep], y[keep])
+
+
+# ---- padded batches -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("new,hq,hkv,d,ps", [([1] * 40 + [380], 4, 2, 128, 64), ([1] * 30 + [400], 8, 4, 64, 16)])
+def test_padding_rows_change_no_bits(P, new, hq, hkv, d, ps):
+    """A chunk beside single tokens: rows behind the batch, as many as make the number of requests divide
+    the number of rows or not, are not a reason to work otherwise."""
+    kv = [n + 50 * (i % 7) for i, n in enumerate(new)]
+    need = [-(-m // ps) for m in kv]
+    at = U.offsets(need)
+    table = i32([list(range(a, a + n)) + [-1] * (max(need) - n) for a, n in zip(at, need)])
+    kc, vc = (rows(i, sum(need), hkv, ps, d).cuda() for i in (2, 3))
+    n, B = sum(new), len(new)
+    up = -(-n // B) * B
+    q = rows(1, hq, up + 2, d).cuda()
+    got = [P.pisa_paged_attention(q[:, :T], kc, vc, table, i32(U.offsets(new)), i32(kv))[:, :n]
+           for T in (up - 1 if up > n else up + 1, up, up + 1, up + 2)]
+    P.pisa_device_status()
+    assert all(torch.equal(x, got[0]) for x in got)
