@@ -13,6 +13,7 @@ import ctypes
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L
 from .api import _check, _require
@@ -238,10 +239,12 @@ def _laid_out(t):
 def varlen_attention(q, k, v, cu_seqlens, causal: bool = True,
                      scale: Optional[float] = None) -> torch.Tensor:
     """Attention over packed sequences, differentiable with respect to q, k and v (bf16; float16
-    without gradients).  Rows that belong to no sequence are zero, and so are their gradients.
+    without gradients; no forward-mode derivative).  Rows that belong to no sequence are zero, and so are their gradients.
     A training step can be captured into a CUDA graph; as with any autograd function, no eager
     autograd graph of the same leaves may be alive then (autograd would make the capture wait for
     the stream that graph was built on)."""
+    if any(forward_ad.unpack_dual(x).tangent is not None for x in (q, k, v)):
+        raise ValueError("varlen_attention has no forward-mode derivative")
     q, k, v = (_laid_out(x) for x in (q, k, v))
     if torch.is_grad_enabled() and any(x.requires_grad for x in (q, k, v)):
         if q.dtype != torch.bfloat16:
