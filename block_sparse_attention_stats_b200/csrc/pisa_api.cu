@@ -318,6 +318,24 @@ static pisa_status launch_select(const float *qbar, const float *kbar, const flo
   return check_launch();
 }
 
+using CtxGetCurrentFn = CUresult (*)(CUcontext *);
+using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long *);
+
+// The calling thread's current context, nullptr where there is none.
+static CUcontext current_context() {
+  static CtxGetCurrentFn get_current = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      get_current = reinterpret_cast<CtxGetCurrentFn>(p);
+  });
+  CUcontext ctx = nullptr;
+  return get_current && get_current(&ctx) == CUDA_SUCCESS ? ctx : nullptr;
+}
+
 // ---- tensor maps for the tensor-memory-accelerator loads ------------------------
 using EncodeTiledFn = PFN_cuTensorMapEncodeTiled_v12000;
 
@@ -333,10 +351,9 @@ EncodeTiledFn encode_tiled() {
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
   // the driver's function wants a current context, which a host thread (autograd's, say) only has
-  // after a runtime call that makes one
-  static thread_local bool ready = false;
+  // after a runtime call that makes one; a thread that has one, of whatever kind, keeps it
   int dev;
-  if (!ready && cudaGetDevice(&dev) == cudaSuccess) ready = cudaSetDevice(dev) == cudaSuccess;
+  if (!current_context() && cudaGetDevice(&dev) == cudaSuccess) cudaSetDevice(dev);
   return fn;
 }
 
@@ -530,31 +547,21 @@ static pisa_status make_map_f32_rows(CUtensorMap *m, const void *base, uint64_t 
   return PISA_OK;
 }
 
-using CtxGetCurrentFn = CUresult (*)(CUcontext *);
-using CtxGetIdFn = CUresult (*)(CUcontext, unsigned long long *);
-
 // Unique id of the calling thread's current context (cuCtxGetId: ids are never
 // reused within a process), or 0 when there is none or the driver lacks the call.
 static unsigned long long current_context_id() {
-  static CtxGetCurrentFn get_current = nullptr;
   static CtxGetIdFn get_id = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      get_current = reinterpret_cast<CtxGetCurrentFn>(p);
-    p = nullptr;
     if (cudaGetDriverEntryPoint("cuCtxGetId", &p, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
       get_id = reinterpret_cast<CtxGetIdFn>(p);
   });
-  if (!get_current || !get_id) return 0;
-  CUcontext ctx = nullptr;
+  CUcontext ctx = current_context();
   unsigned long long id = 0;
-  if (get_current(&ctx) != CUDA_SUCCESS || !ctx) return 0;
-  if (get_id(ctx, &id) != CUDA_SUCCESS) return 0;
+  if (!get_id || !ctx || get_id(ctx, &id) != CUDA_SUCCESS) return 0;
   return id;
 }
 

@@ -237,3 +237,71 @@ def test_padding_rows_change_no_bits(P, new, hq, hkv, d, ps):
            for T in (up - 1 if up > n else up + 1, up, up + 1, up + 2)]
     P.pisa_device_status()
     assert all(torch.equal(x, got[0]) for x in got)
+
+
+# ---- a caller's own context ---------------------------------------------------------------------------
+
+def test_a_callers_context_stays_current(P):
+    """A host thread with a context of its own has it after the call too, and the call works there."""
+    import ctypes
+    import threading
+    from block_sparse_attention_stats_b200 import _lib as L
+
+    torch.zeros(1, device="cuda")
+    cuda, lib = ctypes.CDLL("libcuda.so.1"), L.load()
+    seen, failed = {}, []
+
+    def ok(code):
+        assert code == 0, f"CUresult {code}"
+
+    def current():
+        c = ctypes.c_void_p()
+        ok(cuda.cuCtxGetCurrent(ctypes.byref(c)))
+        return c.value
+
+    def body():
+        mine = ctypes.c_void_p()
+        ok(cuda.cuCtxCreate_v2(ctypes.byref(mine), 0, 0))
+        try:
+            # tensor maps are encoded, and refused (a group's stride past 2^40 bytes): nothing is launched
+            far = L.PisaRows(1 << 20, (1 << 38) - 8, 64)
+            near = L.PisaRows(2 << 20, 6400, 64)
+            seen["status"] = lib.pisa_varlen_attention(
+                far, near, near, L.PISA_BF16, 3 << 20, 1, 100, 8, 2, 64, 0.0, 1, L.PisaRows(4 << 20, 6400, 64), None,
+                None, 5 << 20, 1 << 30, None)
+            seen["kept"] = current() == mine.value
+            if not seen["kept"]:
+                return
+            # one token attends to itself: out = v
+            d, need = 64, lib.pisa_varlen_attention_workspace_bytes(1, 1, 64)
+            at = ctypes.c_uint64()
+            ok(cuda.cuMemAlloc_v2(ctypes.byref(at), ctypes.c_size_t(4096 + need)))
+            q, k, v, out, cu, ws = (at.value + x for x in (0, 256, 512, 768, 1024, 4096))
+            x = (torch.arange(d) / 8).to(BF)
+            for p in (q, k, v):
+                ok(cuda.cuMemcpyHtoD_v2(ctypes.c_uint64(p), ctypes.c_void_p(x.data_ptr()), ctypes.c_size_t(2 * d)))
+            lens = torch.tensor([0, 1], dtype=torch.int32)
+            ok(cuda.cuMemcpyHtoD_v2(ctypes.c_uint64(cu), ctypes.c_void_p(lens.data_ptr()), ctypes.c_size_t(8)))
+            row = lambda p: L.PisaRows(p, d, d)
+            seen["call"] = lib.pisa_varlen_attention(row(q), row(k), row(v), L.PISA_BF16, cu, 1, 1, 1, 1, d, 0.0, 1,
+                                                     row(out), None, None, ws, need, None)
+            ok(cuda.cuCtxSynchronize())
+            got = torch.zeros(d, dtype=BF)
+            ok(cuda.cuMemcpyDtoH_v2(ctypes.c_void_p(got.data_ptr()), ctypes.c_uint64(out), ctypes.c_size_t(2 * d)))
+            seen["out"] = torch.equal(got, x)
+            seen["still"] = current() == mine.value
+            ok(cuda.cuMemFree_v2(at))
+        finally:
+            ok(cuda.cuCtxDestroy_v2(mine))
+
+    def guarded():
+        try:
+            body()
+        except BaseException as e:
+            failed.append(e)
+
+    t = threading.Thread(target=guarded)
+    t.start()
+    t.join()
+    assert not failed, failed
+    assert seen == dict(status=L.PISA_ERR_CUDA, kept=True, call=L.PISA_OK, out=True, still=True)
