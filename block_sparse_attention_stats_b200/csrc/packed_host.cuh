@@ -69,6 +69,110 @@ inline pisa_status check_rows(const pisa_rows &r, int H, int T, int d, bool writ
   return PISA_OK;
 }
 
+// ---- operands that share memory ---------------------------------------------------------
+// The memory of one operand: rows of `size` bytes, n[i] of them stride[i] bytes apart, outermost
+// (widest stride) first, neighbouring dimensions merged where one fills the other's stride, so a
+// dense tensor is one row.  `nested`: no block reaches into the next, so no two rows share memory.
+struct Area {
+  const char *data, *end;   // from the first row to behind the last
+  __int128 size, stride[3], n[3];
+  int dims;
+  bool nested;
+  __int128 span(int from = 0) const {
+    __int128 s = size;
+    for (int i = from; i < dims; ++i) s += (n[i] - 1) * stride[i];
+    return s;
+  }
+};
+inline Area area(const void *data, int64_t bytes) {
+  Area a{};
+  a.data = (const char *)data;
+  a.size = data ? bytes : 0;
+  a.end = a.data + (int64_t)a.size;
+  a.nested = true;
+  return a;
+}
+// counts and strides (elements of two bytes) of `dims` dimensions in any order, over rows of d elements
+inline Area area(const void *data, int d, int dims, const int64_t *n, const int64_t *stride) {
+  Area a = area(data, 2ll * d);
+  for (int i = 0; i < dims; ++i) {
+    if (n[i] <= 0) a.size = 0;
+    if (n[i] <= 1) continue;
+    int at = a.dims++;
+    for (; at > 0 && a.stride[at - 1] < 2 * (__int128)stride[i]; --at) {
+      a.stride[at] = a.stride[at - 1];
+      a.n[at] = a.n[at - 1];
+    }
+    a.stride[at] = 2 * (__int128)stride[i];
+    a.n[at] = n[i];
+  }
+  while (a.dims && a.stride[a.dims - 1] == a.size) a.size *= a.n[--a.dims];
+  __int128 span = a.size;
+  for (int i = a.dims - 1; i >= 0; --i) {
+    a.nested = a.nested && a.stride[i] >= span;
+    span += (a.n[i] - 1) * a.stride[i];
+  }
+  // (past the address space, strides that no memory has: as far as it goes)
+  const __int128 end = (__int128)(uintptr_t)data + span;
+  a.end = (const char *)(end > UINTPTR_MAX ? UINTPTR_MAX : (uintptr_t)end);
+  return a;
+}
+inline Area area(const pisa_rows &r, int H, int T, int d) {
+  const int64_t n[] = {H, T}, s[] = {r.head_stride, r.row_stride};
+  return area(r.data, d, 2, n, s);
+}
+inline Area area(const pisa_pages &c, int pages, int H, int ps, int d) {
+  const int64_t n[] = {pages, H, ps}, s[] = {c.page_stride, c.head_stride, c.row_stride};
+  return area(c.data, d, 3, n, s);
+}
+
+// Whether dimensions i on of a and j on of b, at[b] - at[a] = off, share a byte.  Exact where the outer
+// strides are equal (slices of one tensor) or one of the two is dense; other layouts, whose rows may
+// lie between one another's, count as apart.
+inline bool areas_meet(const Area &a, int i, const Area &b, int j, __int128 off) {
+  if (off >= a.span(i) || -off >= b.span(j)) return false;
+  if (i == a.dims && j == b.dims) return true;
+  auto down = [](__int128 x, __int128 y) { return x / y - (x % y < 0); };
+  if (i < a.dims && j < b.dims) {
+    const __int128 s = a.stride[i];
+    if (s != b.stride[j]) return false;
+    // block x of a and y of b lie off + (y - x) s apart: the few differences k at which they can meet
+    __int128 k0 = down(-off - b.span(j + 1), s) + 1, k1 = down(a.span(i + 1) - 1 - off, s);
+    if (k0 < 1 - a.n[i]) k0 = 1 - a.n[i];
+    if (k1 > b.n[j] - 1) k1 = b.n[j] - 1;
+    for (__int128 k = k0; k <= k1; ++k)
+      if (areas_meet(a, i + 1, b, j + 1, off + k * s)) return true;
+    return false;
+  }
+  if (i < a.dims) return areas_meet(b, j, a, i, -off);
+  // a dense: the blocks of b that reach into it; of three, the middle one lies inside
+  const __int128 s = b.stride[j];
+  __int128 k0 = down(-off - b.span(j + 1), s) + 1, k1 = down(a.span(i) - 1 - off, s);
+  if (k0 < 0) k0 = 0;
+  if (k1 > b.n[j] - 1) k1 = b.n[j] - 1;
+  if (k1 - k0 >= 2) return true;
+  for (__int128 k = k0; k <= k1; ++k)
+    if (areas_meet(a, i, b, j + 1, off + k * s)) return true;
+  return false;
+}
+inline bool share_memory(const Area &a, const Area &b) {
+  if (a.end <= b.data || b.end <= a.data || a.size == 0 || b.size == 0) return false;
+  if (a.data == b.data) return true;
+  if (!a.nested || !b.nested) return false;
+  return areas_meet(a, 0, b, 0, (__int128)(intptr_t)b.data - (__int128)(intptr_t)a.data);
+}
+// What a call writes may share memory neither with what it reads nor with anything else it writes
+// (`from`: those before have been looked at).
+inline pisa_status check_apart(const Area *written, int nw, const Area *read, int nr, int from = 0) {
+  for (int i = from; i < nw; ++i) {
+    for (int j = 0; j < nr; ++j)
+      if (share_memory(written[i], read[j])) return PISA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (share_memory(written[i], written[j])) return PISA_ERR_INVALID_ARG;
+  }
+  return PISA_OK;
+}
+
 // 16-bit tensor of `rank` dimensions, innermost contiguous, read in boxes of 64
 // columns with the 128-byte swizzle; what lies outside reads as zero.
 inline pisa_status map16(CUtensorMap *m, const void *base, bool bf16, int rank, const uint64_t *dims,

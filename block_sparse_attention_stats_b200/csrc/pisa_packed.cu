@@ -171,6 +171,22 @@ static pisa_status check_pages(const pisa_pages &c, int H, int ps, int pages, in
 
 static bool page_size_ok(int ps) { return ps == 16 || ps == 32 || ps == 64 || ps == 128 || ps == 256; }
 
+// What a plan writes, and what every CTA of it reads while others write.
+struct StepWritten {
+  Area a[5];
+};
+struct StepRead {
+  Area a[4];
+};
+static StepWritten step_written(const pisa_page_step &s) {
+  return {{area(s.block_table, 4ll * s.B * s.width), area(s.slots, 8ll * s.T), area(s.cu_seqlens, 4ll * (s.B + 1)),
+           area(s.kv_lens, 4ll * s.B), area(s.num_free_out, 4)}};
+}
+static StepRead step_read(const pisa_page_step &s) {
+  return {{area(s.past_lens, 4ll * s.B), area(s.new_lens, 4ll * s.B), area(s.num_free, 4),
+           area(s.free_pages, 4ll * s.free_cap)}};
+}
+
 static pisa_status check_step(const pisa_page_step *s) {
   if (!s || s->B < 1 || s->T < 0 || s->width < 1 || s->page_size < 1 || s->free_cap < 0)
     return PISA_ERR_INVALID_ARG;
@@ -182,16 +198,7 @@ static pisa_status check_step(const pisa_page_step *s) {
     return PISA_ERR_INVALID_ARG;
   if (s->free_cap && !is_int32(s->free_pages)) return PISA_ERR_INVALID_ARG;
   if (s->T && (!s->slots || ((uintptr_t)s->slots & 7u))) return PISA_ERR_INVALID_ARG;
-  // every CTA reads the lengths, the free list and its count while others write
-  const void *in[] = {s->past_lens, s->new_lens, s->num_free, s->free_pages};
-  const void *out[] = {s->cu_seqlens, s->kv_lens, s->num_free_out, s->block_table, s->slots};
-  for (const void *o : out)
-    for (const void *i : in)
-      if (o && o == i) return PISA_ERR_INVALID_ARG;
-  for (int a = 0; a < 5; ++a)
-    for (int b = 0; b < a; ++b)
-      if (out[a] && out[a] == out[b]) return PISA_ERR_INVALID_ARG;
-  return PISA_OK;
+  return check_apart(step_written(*s).a, 5, step_read(*s).a, 4);
 }
 
 }  // namespace pisa
@@ -217,11 +224,16 @@ pisa_status pisa_varlen_attention(pisa_rows q, pisa_rows k, pisa_rows v, pisa_dt
   PISA_TRY(check_rows(k, Hkv, T, d, false));
   PISA_TRY(check_rows(v, Hkv, T, d, false));
   PISA_TRY(check_rows(out, Hq, T, d, true));
-  if (out.data == q.data || out.data == k.data || out.data == v.data) return PISA_ERR_INVALID_ARG;
   if (lse && !is_int32(lse)) return PISA_ERR_INVALID_ARG;
-  if (out_f32 && (!aligned16(out_f32) || (void *)out_f32 == out.data)) return PISA_ERR_INVALID_ARG;
+  if (out_f32 && !aligned16(out_f32)) return PISA_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
-  if (ws_bytes < packed_scratch(d, 256).total) return PISA_ERR_WORKSPACE;
+  const size_t need = packed_scratch(d, 256).total;
+  const Area read[] = {area(q, Hq, T, d), area(k, Hkv, T, d), area(v, Hkv, T, d), area(cu_seqlens, 4ll * (B + 1))};
+  const Area written[] = {area(out, Hq, T, d), area(lse, 4ll * Hq * T), area(out_f32, 4ll * Hq * T * d),
+                          area(workspace, need)};
+  PISA_TRY(check_apart(written, 3, read, 4));
+  if (ws_bytes < need) return PISA_ERR_WORKSPACE;
+  PISA_TRY(check_apart(written, 4, read, 4, 3));
   const PackedProblem p = problem(cu_seqlens, nullptr, B, T, Hq, Hkv, flags & PISA_CAUSAL, T);
   const PackedOut o{out.data, out.head_stride, out.row_stride, lse, out_f32};
   const int clear = flags & PISA_ZERO_TAIL;
@@ -254,10 +266,19 @@ pisa_status pisa_paged_attention(pisa_rows q, pisa_pages k_cache, pisa_pages v_c
   PISA_TRY(check_rows(out, Hq, T, d, true));
   PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d));
   PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d));
-  if (out.data == q.data || out.data == k_cache.data || out.data == v_cache.data) return PISA_ERR_INVALID_ARG;
   if (lse && !is_int32(lse)) return PISA_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
-  if (ws_bytes < packed_scratch(d, 256).total) return PISA_ERR_WORKSPACE;
+  const size_t need = packed_scratch(d, 256).total;
+  const Area read[] = {area(q, Hq, T, d),
+                       area(k_cache, num_pages, Hkv, page_size, d),
+                       area(v_cache, num_pages, Hkv, page_size, d),
+                       area(block_table, 4ll * B * width),
+                       area(cu_seqlens, 4ll * (B + 1)),
+                       area(kv_lens, 4ll * B)};
+  const Area written[] = {area(out, Hq, T, d), area(lse, 4ll * Hq * T), area(workspace, need)};
+  PISA_TRY(check_apart(written, 2, read, 6));
+  if (ws_bytes < need) return PISA_ERR_WORKSPACE;
+  PISA_TRY(check_apart(written, 3, read, 6, 2));
   const PackedProblem p = problem(cu_seqlens, kv_lens, B, T, Hq, Hkv, 1, (long long)width * page_size);
   const PagedKV cache{block_table, width, page_size, num_pages};
   const PackedOut o{out.data, out.head_stride, out.row_stride, lse, nullptr};
@@ -308,11 +329,9 @@ pisa_status pisa_page_write(pisa_rows k, pisa_rows v, pisa_dtype dtype, const in
   PISA_TRY(check_rows(v, Hkv, T, d, false));
   PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d));
   PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d));
-  const void *src[2] = {k.data, v.data}, *dst[2] = {k_cache.data, v_cache.data};
-  if (dst[0] == dst[1]) return PISA_ERR_INVALID_ARG;
-  for (const void *a : src)
-    for (const void *b : dst)
-      if (a == b) return PISA_ERR_INVALID_ARG;
+  const Area read[] = {area(k, Hkv, T, d), area(v, Hkv, T, d), area(slots, 8ll * T)};
+  const Area written[] = {area(k_cache, num_pages, Hkv, page_size, d), area(v_cache, num_pages, Hkv, page_size, d)};
+  PISA_TRY(check_apart(written, 2, read, 3));
   PageWrite w{};
   const pisa_rows r[2] = {k, v};
   const pisa_pages c[2] = {k_cache, v_cache};
@@ -353,13 +372,17 @@ pisa_status pisa_paged_step(const pisa_page_step *step, pisa_rows q, pisa_rows k
     PISA_TRY(check_rows(out, Hq, T, d, true));
     PISA_TRY(check_pages(k_cache, Hkv, ps, num_pages, d));
     PISA_TRY(check_pages(v_cache, Hkv, ps, num_pages, d));
-    const void *src[3] = {q.data, k.data, v.data}, *dst[3] = {k_cache.data, v_cache.data, out.data};
-    for (const void *a : src)
-      for (const void *b : dst)
-        if (a == b) return PISA_ERR_INVALID_ARG;
-    if (dst[0] == dst[1] || dst[0] == dst[2] || dst[1] == dst[2]) return PISA_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
-    if (ws_bytes < packed_scratch(d, 256).total) return PISA_ERR_WORKSPACE;
+    const size_t need = packed_scratch(d, 256).total;
+    const StepRead sr = step_read(*step);
+    const StepWritten sw = step_written(*step);
+    const Area read[] = {sr.a[0], sr.a[1], sr.a[2], sr.a[3], area(q, Hq, T, d), area(k, Hkv, T, d), area(v, Hkv, T, d)};
+    const Area written[] = {sw.a[0], sw.a[1], sw.a[2], sw.a[3], sw.a[4],
+                            area(k_cache, num_pages, Hkv, ps, d), area(v_cache, num_pages, Hkv, ps, d),
+                            area(out, Hq, T, d), area(lse, 4ll * Hq * T), area(workspace, need)};
+    PISA_TRY(check_apart(written, 9, read, 7));
+    if (ws_bytes < need) return PISA_ERR_WORKSPACE;
+    PISA_TRY(check_apart(written, 10, read, 7, 9));
   }
   PISA_TRY(pisa_page_plan(step, stream));
   PISA_TRY(pisa_page_write(k, v, dtype, step->slots, T, Hkv, d, k_cache, v_cache, num_pages, ps, stream));

@@ -124,13 +124,14 @@ pisa_status pisa_varlen_attention_bwd(pisa_rows q, pisa_rows k, pisa_rows v, pis
   PISA_TRY(check_rows(dk, Hkv, T, d, true));
   PISA_TRY(check_rows(dv, Hkv, T, d, true));
   if (!lse || ((uintptr_t)lse & 3u) || !aligned16(out_f32) || !aligned16(workspace)) return PISA_ERR_INVALID_ARG;
-  const void *in[] = {q.data, k.data, v.data, dout.data, out_f32, lse};
-  const void *out[] = {dq.data, dk.data, dv.data};
-  for (const void *o : out)
-    for (const void *i : in)
-      if (o == i) return PISA_ERR_INVALID_ARG;
-  if (out[0] == out[1] || out[0] == out[2] || out[1] == out[2]) return PISA_ERR_INVALID_ARG;
-  if (ws_bytes < packed_bwd_layout(T, Hq, d).total) return PISA_ERR_WORKSPACE;
+  const size_t need = packed_bwd_layout(T, Hq, d).total;
+  const Area read[] = {area(q, Hq, T, d),           area(k, Hkv, T, d),  area(v, Hkv, T, d),
+                       area(dout, Hq, T, d),        area(lse, 4ll * Hq * T), area(out_f32, 4ll * Hq * T * d),
+                       area(cu_seqlens, 4ll * (B + 1))};
+  const Area written[] = {area(dq, Hq, T, d), area(dk, Hkv, T, d), area(dv, Hkv, T, d), area(workspace, need)};
+  PISA_TRY(check_apart(written, 3, read, 7));
+  if (ws_bytes < need) return PISA_ERR_WORKSPACE;
+  PISA_TRY(check_apart(written, 4, read, 7, 3));
   PackedProblem p{};
   p.cu = cu_seqlens;
   p.B = B;

@@ -310,6 +310,10 @@ size_t pisa_dense_attention_workspace_bytes(int B, int H, int L, int d, pisa_dty
  *    sequence's last key may hold anything, NaN included.  A non-finite key or
  *    value inside a sequence may reach any row of that sequence (and head
  *    group), masked or not, but no other sequence.
+ *  - What a call writes (its workspace included) shares memory with nothing else
+ *    that it is given.  That is refused where the layouts show it: equal outer
+ *    strides, as of slices of one tensor, or one of the two dense.  Elsewhere it
+ *    is the caller's care, and results are unspecified.
  *  - Results do not depend on timing: no atomics, a fixed order of every sum.
  *    `workspace` is scratch of one call; calls that may overlap need one each. */
 typedef struct {
@@ -337,7 +341,7 @@ size_t pisa_varlen_attention_workspace_bytes(int Hq, int Hkv, int d);
  *   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(s q_t . k_j)
  * q, out: [Hq][T]; k, v: [Hkv][T].  lse (may be NULL): float32 [Hq, T], ln of
  * the sum.  out_f32 (may be NULL; 16-byte aligned): float32 [Hq, T, d], the
- * output before its rounding, which the backward needs.  out overlaps no input. */
+ * output before its rounding, which the backward needs. */
 pisa_status pisa_varlen_attention(pisa_rows q, pisa_rows k, pisa_rows v, pisa_dtype dtype,
                                   const int32_t *cu_seqlens, int B, int T, int Hq, int Hkv, int d,
                                   float scale, int flags, pisa_rows out, float *lse, float *out_f32,
@@ -350,8 +354,7 @@ size_t pisa_varlen_attention_bwd_workspace_bytes(int T, int Hq, int Hkv, int d);
  * Delta) has no scale of its own and would underflow in f16.  lse and out_f32
  * from one forward call on the same inputs that was given both (its output is
  * then divided by the sum of the rounded weights, which the backward needs; lse is
- * the sum's before rounding either way).  dq, dk, dv
- * overlap no input and one another not. */
+ * the sum's before rounding either way). */
 pisa_status pisa_varlen_attention_bwd(pisa_rows q, pisa_rows k, pisa_rows v, pisa_rows dout,
                                       pisa_dtype dtype, const float *lse, const float *out_f32,
                                       const int32_t *cu_seqlens, int B, int T, int Hq, int Hkv,
@@ -394,14 +397,12 @@ typedef struct {
  * requests take theirs in order.  All or nothing: if a length is negative, a
  * request outgrows the table's width, the new tokens outgrow T or the pages run
  * out, the table and the counts stay as they are, every slot is -1, cu_seqlens
- * is all 0, kv_lens = past_lens, and the status word records it.  Outputs
- * overlap no input and no other output (the table aside, which is both). */
+ * is all 0, kv_lens = past_lens, and the status word records it. */
 pisa_status pisa_page_plan(const pisa_page_step *step, pisa_stream_t stream);
 
 /* Rows t of k and v (packed, [Hkv][T]) to their slots of the caches; rows with a
  * negative slot are left out, a slot past the caches is left out and recorded.
- * Slots are distinct (rows of equal slots leave an unspecified mix).  The caches
- * overlap neither k, v nor one another. */
+ * Slots are distinct (rows of equal slots leave an unspecified mix). */
 pisa_status pisa_page_write(pisa_rows k, pisa_rows v, pisa_dtype dtype, const int64_t *slots, int T,
                             int Hkv, int d, pisa_pages k_cache, pisa_pages v_cache, int num_pages,
                             int page_size, pisa_stream_t stream);

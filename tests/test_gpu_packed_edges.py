@@ -305,3 +305,26 @@ def test_a_callers_context_stays_current(P):
     t.join()
     assert not failed, failed
     assert seen == dict(status=L.PISA_ERR_CUDA, kept=True, call=L.PISA_OK, out=True, still=True)
+
+
+# ---- operands that lie between one another -----------------------------------------------------------
+
+@pytest.mark.parametrize("tokens_first", [False, True])
+def test_a_step_on_slices_of_one_projection_and_one_cache(P, tokens_first):
+    """q, k, v of one fused tensor, out beside them, keys and values of two layers in one cache tensor."""
+    hq, hkv, d, ps, total = 4, 2, 64, 16, 20
+    new = [30, 1, 70]
+    T = sum(new)
+    fused = rows(1, T, 2 * hq + 2 * hkv, d).cuda().transpose(0, 1)
+    q, k, v, out = fused[:hq], fused[hq:hq + hkv], fused[hq + hkv:hq + 2 * hkv], fused[hq + 2 * hkv:]
+    shape = (total, 4, ps, hkv, d) if tokens_first else (total, 4, hkv, ps, d)
+    both = torch.full(shape, 7.0, dtype=BF, device="cuda")
+    kc, vc = (both[:, i].transpose(1, 2) if tokens_first else both[:, i] for i in (1, 2))
+    sep = [torch.full((total, hkv, ps, d), 7.0, dtype=BF, device="cuda") for _ in range(2)]
+    args = lambda: (i32([0, 0, 0]), i32(new), torch.full((3, 6), -1, dtype=torch.int32, device="cuda"),
+                    i32(list(range(total))), i32([total]))
+    want, _ = P.pisa_paged_step(q.contiguous(), k.contiguous(), v.contiguous(), *sep, *args())
+    got, _ = P.pisa_paged_step(q, k, v, kc, vc, *args(), out=out)
+    P.pisa_device_status()
+    assert torch.equal(got, want) and torch.equal(kc, sep[0]) and torch.equal(vc, sep[1])
+    assert (both[:, 0] == 7).all() and (both[:, 3] == 7).all()
