@@ -160,12 +160,14 @@ static PackedProblem problem(const int32_t *cu, const int32_t *kv_lens, int B, i
 
 static bool is_int32(const void *p) { return p && ((uintptr_t)p & 3u) == 0; }
 
-static pisa_status check_pages(const pisa_pages &c, int H, int ps, int pages, int d) {
+// (rows of a cache that is written must not share memory)
+static pisa_status check_pages(const pisa_pages &c, int H, int ps, int pages, int d, bool written) {
   if (!aligned16(c.data)) return PISA_ERR_INVALID_ARG;
   const int64_t s[3] = {c.page_stride, c.head_stride, c.row_stride};
   const int n[3] = {pages, H, ps};
   for (int i = 0; i < 3; ++i)
     if (n[i] > 1 && (s[i] < d || s[i] % 8 || s[i] >= (1ll << 38))) return PISA_ERR_INVALID_ARG;
+  if (written && !area(c, pages, H, ps, d).nested) return PISA_ERR_INVALID_ARG;
   return PISA_OK;
 }
 
@@ -264,8 +266,8 @@ pisa_status pisa_paged_attention(pisa_rows q, pisa_pages k_cache, pisa_pages v_c
   if (T == 0) return PISA_OK;
   PISA_TRY(check_rows(q, Hq, T, d, false));
   PISA_TRY(check_rows(out, Hq, T, d, true));
-  PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d));
-  PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d));
+  PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d, false));
+  PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d, false));
   if (lse && !is_int32(lse)) return PISA_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
   const size_t need = packed_scratch(d, 256).total;
@@ -327,8 +329,8 @@ pisa_status pisa_page_write(pisa_rows k, pisa_rows v, pisa_dtype dtype, const in
   if (!slots || ((uintptr_t)slots & 7u)) return PISA_ERR_INVALID_ARG;
   PISA_TRY(check_rows(k, Hkv, T, d, false));
   PISA_TRY(check_rows(v, Hkv, T, d, false));
-  PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d));
-  PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d));
+  PISA_TRY(check_pages(k_cache, Hkv, page_size, num_pages, d, true));
+  PISA_TRY(check_pages(v_cache, Hkv, page_size, num_pages, d, true));
   const Area read[] = {area(k, Hkv, T, d), area(v, Hkv, T, d), area(slots, 8ll * T)};
   const Area written[] = {area(k_cache, num_pages, Hkv, page_size, d), area(v_cache, num_pages, Hkv, page_size, d)};
   PISA_TRY(check_apart(written, 2, read, 3));
@@ -370,8 +372,8 @@ pisa_status pisa_paged_step(const pisa_page_step *step, pisa_rows q, pisa_rows k
     PISA_TRY(check_rows(k, Hkv, T, d, false));
     PISA_TRY(check_rows(v, Hkv, T, d, false));
     PISA_TRY(check_rows(out, Hq, T, d, true));
-    PISA_TRY(check_pages(k_cache, Hkv, ps, num_pages, d));
-    PISA_TRY(check_pages(v_cache, Hkv, ps, num_pages, d));
+    PISA_TRY(check_pages(k_cache, Hkv, ps, num_pages, d, true));
+    PISA_TRY(check_pages(v_cache, Hkv, ps, num_pages, d, true));
     if (!aligned16(workspace)) return PISA_ERR_INVALID_ARG;
     const size_t need = packed_scratch(d, 256).total;
     const StepRead sr = step_read(*step);

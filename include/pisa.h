@@ -323,7 +323,8 @@ typedef struct {
 
 /* [num_pages][Hkv][page_size] rows of d elements: position j of a request is
  * row j % page_size of page block_table[j / page_size].  page_size is 16, 32,
- * 64, 128 or 256.  Alignment and strides as for pisa_rows. */
+ * 64, 128 or 256.  Alignment and strides as for pisa_rows; rows of a cache that is
+ * written do not share memory (refused, as for packed tensors that are written). */
 typedef struct {
   void *data;
   int64_t page_stride, head_stride, row_stride; /* elements */

@@ -178,3 +178,25 @@ def test_steps_that_do_not(lib):
     assert whole(lib, q=tokens(FUSED - 512 * MB, N), k=tokens(FUSED - 512 * MB + HQ * ROW, N),
                  v=tokens(FUSED - 512 * MB + (HQ + HKV) * ROW, N), kc=pages(A[3], p=2 * HKV * PS * D),
                  vc=pages(A[3] + PAGE, p=2 * HKV * PS * D)) == WORKSPACE
+
+
+# caches whose heads, pages or rows reach into one another: [pages, heads, page size] strides
+SELF = [dict(p=PS * D, h=PS * D), dict(h=PS * D - 8), dict(p=HKV * PS * D - 8), dict(p=D, h=P * D, r=2 * D),
+        dict(r=2 * D), dict(p=2 * HKV * PS * D, h=2 * HKV * PS * D, r=D)]
+APART = [dict(), dict(p=HKV * PS * D, h=D, r=HKV * D), dict(p=4 * HKV * PS * D), dict(p=D, h=P * D, r=P * HKV * D),
+         dict(p=2 * HKV * PS * D, h=2 * PS * D, r=2 * D), dict(p=PS * D, h=P * PS * D)]
+
+
+@pytest.mark.parametrize("strides", SELF)
+def test_a_cache_that_meets_itself_is_not_written(lib, strides):
+    for kc, vc in ((pages(A[3], **strides), pages(A[4])), (pages(A[3]), pages(A[4], **strides))):
+        assert lib.pisa_page_write(heads(A[0]), heads(A[1]), L.PISA_BF16, A[5], T, HKV, D, kc, vc, P, PS,
+                                   None) == INVALID
+        assert whole(lib, kc=kc, vc=vc) == INVALID
+    # reading it does no harm
+    assert paged(lib, kc=pages(A[1], **strides)) == WORKSPACE
+
+
+@pytest.mark.parametrize("strides", APART)
+def test_a_cache_that_does_not_is(lib, strides):
+    assert whole(lib, kc=pages(A[3], **strides), vc=pages(A[4], **strides)) == WORKSPACE
