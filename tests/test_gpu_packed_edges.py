@@ -328,3 +328,46 @@ def test_a_step_on_slices_of_one_projection_and_one_cache(P, tokens_first):
     P.pisa_device_status()
     assert torch.equal(got, want) and torch.equal(kc, sep[0]) and torch.equal(vc, sep[1])
     assert (both[:, 0] == 7).all() and (both[:, 3] == 7).all()
+
+
+# ---- the backward's contract ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", [0.3, 1.0, 0.02])
+@pytest.mark.parametrize("d,causal", [(64, True), (128, True), (128, False)])
+def test_gradients_of_an_explicit_scale(P, scale, d, causal):
+    lens, hq, hkv = [300, 41, 1], 6, 2
+    T = sum(lens)
+    q, k, v, g = (rows(i, h, T, d) for i, h in ((1, hq), (2, hkv), (3, hkv), (4, hq)))
+    want, bound = U.varlen_grads(*(x.double() for x in (q, k, v, g)), lens, causal, scale, BF)
+    leaves = [x.cuda().requires_grad_() for x in (q, k, v)]
+    got = torch.autograd.grad(P.varlen_attention(*leaves, i32(U.offsets(lens)), causal, scale), leaves, g.cuda())
+    P.pisa_device_status()
+    for name, x in zip(("dq", "dk", "dv"), got):
+        U.check(x, want[name], bound[name], f"{name} at scale {scale}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[3000, 5, 700], [130, 40]])
+def test_backward_into_slices_of_one_gradient(P, lens, d):
+    """dq, dk, dv as slices of one [T, Hq + 2 Hkv, d] tensor, long enough that ranges cut units; rows of no
+    sequence keep what they held."""
+    hq, hkv, pad, first = 4, 2, 9, 3
+    n = sum(lens)
+    T = first + n + pad
+    q, k, v, g = (rows(i, h, T, d) for i, h in ((1, hq), (2, hkv), (3, hkv), (4, hq)))
+    cu = i32([first + x for x in U.offsets(lens)])
+    dev = [x.cuda() for x in (q, k, v, g)]
+    lse, o32 = torch.empty(hq, T, device="cuda"), torch.empty(hq, T, d, device="cuda")
+    P.pisa_varlen_attention(*dev[:3], cu, lse=lse, out_f32=o32)
+    fused = torch.full((T, hq + 2 * hkv, d), 7.0, dtype=BF, device="cuda").transpose(0, 1)
+    parts = (fused[:hq], fused[hq:hq + hkv], fused[hq + hkv:])
+    got = P.pisa_varlen_attention_bwd(*dev, lse, o32, cu, grads=parts)
+    dense = P.pisa_varlen_attention_bwd(*dev, lse, o32, cu,
+                                        grads=tuple(torch.full_like(x, 7.0) for x in dev[:3]))
+    P.pisa_device_status()
+    r = slice(first, first + n)
+    want, bound = U.varlen_grads(*(x[:, r].double() for x in (q, k, v, g)), lens, True, d ** -0.5, BF)
+    for name, x, y, z in zip(("dq", "dk", "dv"), got, dense, parts):
+        assert x is z and torch.equal(x, y)
+        U.check(x[:, r], want[name], bound[name], name)
+        assert (x[:, :first] == 7).all() and (x[:, first + n:] == 7).all()
