@@ -243,7 +243,7 @@ template <class Cost> struct PackedWalk {
           s.h = 0;
           if (++s.rt >= Cost::units(p, s.r.n)) {
             s.rt = 0;
-            bool bad;
+            bool bad = false;   // (packed_locate has recorded it)
             do {
               if (++s.b >= p.B) return false;   // cannot happen while positions are left
               s.r = packed_request(p, s.b, bad);
