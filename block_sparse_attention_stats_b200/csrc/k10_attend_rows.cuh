@@ -236,9 +236,7 @@ __global__ void __launch_bounds__(RowsCfg<D, R>::kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int row = 16 * i + g + 8 * x;
-        lim[i][x] = row >= rows ? 0
-                    : p.causal  ? max(min(s.r.past + tok0 + row / p.G + 1, s.r.kv), 0)
-                                : s.r.kv;
+        lim[i][x] = row >= rows ? 0 : max(min(s.r.past + tok0 + row / p.G + 1, s.r.kv), 0);
       }
     float m[RT][2], l[RT][2], acc[RT][NT][4];
 #pragma unroll
