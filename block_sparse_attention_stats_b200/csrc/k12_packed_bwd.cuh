@@ -635,7 +635,7 @@ template <int D> __global__ void __launch_bounds__(128) packed_sum_kernel(const 
                     (long long)gridDim.x * gridDim.y * blockDim.x);
   const PackedCut cut = packed_cut_at(a.cuts[kv], blockIdx.x);
   if (!cut.valid) return;
-  bool bad = false;
+  int bad = 0;
   const PackedRequest r = packed_request(p, cut.b, bad);
   const int per = kv ? 128 : p.tq, g = kv ? 1 : p.G, tok0 = cut.rt * per;
   const int rows = min(r.n - tok0, per) * g;

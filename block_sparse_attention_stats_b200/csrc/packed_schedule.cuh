@@ -49,8 +49,9 @@ struct PackedRequest {
 };
 
 // Offsets and lengths are device data: whatever they hold, rows stay inside
-// [0, T) and positions inside [0, max_kv]; `bad` is set where they did not.
-__device__ __forceinline__ PackedRequest packed_request(const PackedProblem &p, int b, bool &bad) {
+// [0, T) and positions inside [0, max_kv]; `bad` says where they did not.
+enum : int { kBadOffsets = 1, kBadLengths = 2 };
+__device__ __forceinline__ PackedRequest packed_request(const PackedProblem &p, int b, int &bad) {
   PackedRequest r;
   const int lo = sm100::ld_int(p.cu + b), hi = sm100::ld_int(p.cu + b + 1);
   const int kv = p.kv_lens ? sm100::ld_int(p.kv_lens + b) : 0;
@@ -58,7 +59,7 @@ __device__ __forceinline__ PackedRequest packed_request(const PackedProblem &p, 
   r.n = max(min(hi, p.T) - r.first, 0);
   r.kv = p.kv_lens ? min(max(kv, 0), p.max_kv) : r.n;
   r.past = r.kv - r.n;
-  bad = bad || lo < 0 || hi < lo || hi > p.T || kv < 0 || kv > p.max_kv;
+  bad |= (lo < 0 || hi < lo || hi > p.T ? kBadOffsets : 0) | (kv < 0 || kv > p.max_kv ? kBadLengths : 0);
   return r;
 }
 
@@ -143,14 +144,16 @@ __device__ __forceinline__ void packed_point(const PackedProblem &p, const Packe
 }
 
 // One call by all `threads` threads of a CTA (a multiple of 32, at most 512):
-// fills *out (shared memory).  Contains two CTA barriers.
+// fills *out (shared memory).  Contains two CTA barriers.  Where offsets are out of order or
+// range nothing is worked on: clamped one by one, B of them could each name all T rows, and a
+// launch take B times as long as a batch of that size (minutes, of a buffer that was never filled).
 template <class Cost>
 __device__ __forceinline__ void packed_locate(const PackedProblem &p, int cta, int grid, int tid, int threads,
                                               long long *warp_sum, PackedStart *out) {
   const int per = (p.B + threads - 1) / threads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long own = 0;
-  bool bad = false;
+  int bad = 0;
   PackedRequest r{};
   for (int b = b0; b < b1; ++b) {
     r = packed_request(p, b, bad);
@@ -165,7 +168,7 @@ __device__ __forceinline__ void packed_locate(const PackedProblem &p, int cta, i
     if (lane >= o) incl += v;
   }
   if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
+  const bool skip = __syncthreads_or(bad & kBadOffsets);
   // sums of the warps before this one, and of all
   long long sum = lane < warps ? warp_sum[lane] : 0;
 #pragma unroll
@@ -173,7 +176,7 @@ __device__ __forceinline__ void packed_locate(const PackedProblem &p, int cta, i
     const long long v = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += v;
   }
-  const long long total = __shfl_sync(0xffffffffu, sum, warps - 1);
+  const long long all = __shfl_sync(0xffffffffu, sum, warps - 1), total = skip ? 0 : all;
   const long long up_to = __shfl_sync(0xffffffffu, sum, max(warp - 1, 0));
   const long long before = (warp ? up_to : 0) + incl - own;
   long long chunk = (long long)((double)total * (1.0 / grid)) + 1;
@@ -243,7 +246,7 @@ template <class Cost> struct PackedWalk {
           s.h = 0;
           if (++s.rt >= Cost::units(p, s.r.n)) {
             s.rt = 0;
-            bool bad = false;   // (packed_locate has recorded it)
+            int bad = 0;   // (packed_locate has recorded it)
             do {
               if (++s.b >= p.B) return false;   // cannot happen while positions are left
               s.r = packed_request(p, s.b, bad);
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(128)
                     (long long)gridDim.x * gridDim.y * blockDim.x);
   const PackedCut cut = packed_cut_at(cuts, blockIdx.x);
   if (!cut.valid) return;
-  bool bad = false;
+  int bad = 0;
   const PackedRequest r = packed_request(p, cut.b, bad);
   const int tok0 = cut.rt * p.tq, rows = min(r.n - tok0, p.tq) * p.G;
   const size_t slot = packed_slot_floats<D>(R);

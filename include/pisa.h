@@ -305,7 +305,8 @@ size_t pisa_dense_attention_workspace_bytes(int B, int H, int L, int d, pisa_dty
  *    whatever they hold at replay.  What is out of range is clamped or left
  *    out, never followed out of bounds, and recorded in the status word
  *    (PISA_ERR_DEVICE from pisa_device_status); results of such a call are
- *    unspecified.
+ *    unspecified.  Of a batch whose cu_seqlens are out of order or range, no
+ *    sequence is worked on.
  *  - A row that sees no key is zero, its lse is -infinity.  Memory behind a
  *    sequence's last key may hold anything, NaN included.  A non-finite key or
  *    value inside a sequence may reach any row of that sequence (and head

@@ -371,3 +371,36 @@ def test_backward_into_slices_of_one_gradient(P, lens, d):
         assert x is z and torch.equal(x, y)
         U.check(x[:, r], want[name], bound[name], name)
         assert (x[:, :first] == 7).all() and (x[:, first + n:] == 7).all()
+
+
+# ---- offsets that are none ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("cu", [[0, 300] * 40, [0, 100, 50, 300], [0, 100, 301], [-1, 100, 300], [300, 0]])
+def test_nothing_is_worked_on_with_bad_offsets(P, cu):
+    """Each pair could name every row: the work of such a call is bounded because there is none."""
+    from block_sparse_attention_stats_b200 import _lib as L
+    T, hq, hkv, d, ps = 300, 4, 2, 64, 16
+    q, k, v, g = (rows(i, h, T, d).cuda() for i, h in ((1, hq), (2, hkv), (3, hkv), (4, hq)))
+    kept = lambda x: torch.full_like(x, 7.0)
+    out, grads = kept(q), tuple(kept(x) for x in (q, k, v))
+    lse, o32 = torch.zeros(hq, T, device="cuda"), torch.zeros(hq, T, d, device="cuda")
+    kc, vc = (pages_of(x.cpu(), ps).cuda() for x in (k, v))
+    B = len(cu) - 1
+    paged, few = kept(q), kept(q[:, :B])
+    table, kv = i32([list(range(kc.shape[0]))] * B), i32([T] * B)
+
+    def refused():
+        with pytest.raises(P.PisaError) as e:
+            P.pisa_device_status()
+        assert e.value.status == L.PISA_ERR_DEVICE
+
+    P.pisa_varlen_attention(q, k, v, i32(cu), out=out)
+    refused()
+    P.pisa_varlen_attention_bwd(q, k, v, g, lse, o32, i32(cu), grads=grads)
+    refused()
+    P.pisa_paged_attention(q, kc, vc, table, i32(cu), kv, out=paged)
+    refused()
+    P.pisa_paged_attention(q[:, :B], kc, vc, table, i32([c // 100 if c > 99 else c for c in cu[:-1]] + [B + 1]), kv, out=few)
+    refused()
+    for x in (out, paged, few, *grads):
+        assert (x == 7).all()
