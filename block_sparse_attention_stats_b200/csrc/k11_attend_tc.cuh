@@ -97,8 +97,9 @@ __device__ __forceinline__ SubTile subtile(const PackedProblem &p, const PackedS
 // back as 16 bits over the scores' first 32 columns, O rescaled where the maximum
 // has moved (once `pv_done` says that the product before is in it).  `seen` columns
 // are visible; SPREAD: those whose key, 16 (c / 8) + c % 8, is below `seen`.
-// A quarter of the exponentials as a polynomial on the multiply-add units did not
-// pay (918 against 893 us on 12000 + 700 + 4608 causal tokens).
+// All exponentials are on the special-function units.  (A quarter of them as a polynomial on
+// the multiply-add units took 918 against 893 us on 12000 + 700 + 4608 causal tokens in an
+// earlier form of this kernel, with whole tiles and one issuing warp; not measured in this one.)
 // The sum is of the float32 weights.  ROUNDED (where the float32 output is wanted
 // too): for the backward the output is divided by the sum of the rounded weights:
 // dout_t . o_t is then the mean of dP under the weights themselves, and does not lose

@@ -5,19 +5,20 @@
 // packed prompts kv = n).  A unit is (sequence, row tile, key head): tq tokens
 // times the G query heads of the key head, G rows a token, against the key
 // positions that the tile's last token sees, in tiles of 128.  All units, each as
-// long as its positions, are laid end to end, and the line is cut into equal
-// ranges, one a CTA, so every CTA gets the same number of tiles (to within one)
-// whatever the lengths are.  Nothing is read on the host: the cut depends on
-// lengths in device memory alone, and the grid on the device alone, so a captured
-// launch serves any lengths.
+// long as its positions and a constant (unit_cost), are laid end to end, and the
+// line is cut into ranges of equal length, one a CTA; a cut counts for the tile that
+// it falls into, in a short unit for the unit's nearer end.  So CTAs get equal
+// lengths to within a tile or a short unit, not equal numbers of tiles: many short units
+// have fewer than one long one, and where there is little work (min_range) some CTAs
+// have none.  Nothing is read on the host: the cut depends on lengths in device
+// memory alone, and the grid on the device alone, so a captured launch serves any
+// lengths.
 // Lengths in positions, not in tiles, make what lies before a unit a polynomial of
-// its number, so a CTA finds its place with a few multiplications; a cut counts
-// for the tile that it falls into.  (Exact sums of rounded tiles, with 64-bit
-// divisions, took 4 us at the start of every kernel.)
+// its number, so a CTA finds its place with a few multiplications.  (Exact sums of
+// rounded tiles, with 64-bit divisions, took 4 us at the start of every kernel.)
 // A unit counts unit_cost positions more than it has, for what its start and its
 // end take: without, a CTA that got many short units ran twice as long as the
-// others.  A cut that falls into these is one at the unit's start, and one in a
-// short unit moves to its nearer end.
+// others.  A cut that falls into these is one at the unit's start.
 // A unit inside one range is written by its CTA.  A unit cut by a range's end
 // leaves float32 partial sums, and packed_combine_kernel joins them in ascending
 // CTA order (no atomics: the same inputs give the same bits).

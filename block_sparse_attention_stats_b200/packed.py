@@ -6,6 +6,8 @@ are [H, T, d] with d contiguous and any head and row strides that are multiples
 of 8 (a [T, H, d] tensor is passed as its transpose(0, 1), a slice of a fused
 projection as it is); caches are [num_pages, Hkv, page_size, d] likewise.  The
 work runs on the tensors' device, on `stream` or that device's current stream.
+A `scale` of None or 0 is 1 / sqrt(d), as in the C calls.  varlen_attention is
+differentiable; results of the pisa_ calls carry no graph.
 """
 from __future__ import annotations
 

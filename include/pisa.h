@@ -300,7 +300,9 @@ size_t pisa_dense_attention_workspace_bytes(int B, int H, int L, int d, pisa_dty
  *    (gradients: PISA_BF16); scores, maxima, sums and accumulators are float32,
  *    softmax weights are rounded to dtype for their product with the values.
  *    (f16: of a weight below 2^-25 of the row's largest, less than the type's
- *    precision is left; below 2^-36 it vanishes.)
+ *    precision is left; below 2^-36 it vanishes.)  Scaled scores of any size that
+ *    float32 holds give finite outputs; gradients need them below 2^23, where it
+ *    still tells one from the next.
  *  - Lengths, offsets and tables stay on the device: a captured call serves
  *    whatever they hold at replay.  What is out of range is clamped or left
  *    out, never followed out of bounds, and recorded in the status word
